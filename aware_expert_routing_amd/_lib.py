@@ -23,6 +23,8 @@ MOE_RES_FORCE_UPDATE, MOE_RES_WAIT = 1, 2
 MOE_ROUTE_TOPK, MOE_ROUTE_OEA, MOE_ROUTE_PRUNED = 0, 1, 2
 MOE_DT_F32, MOE_DT_BF16 = 0, 1
 MOE_W_F32, MOE_W_BF16, MOE_W_INT4_G128 = 0, 1, 2
+MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
+MOE_GROUP_MAX, MOE_GROUP_TOP2 = 0, 1
 
 
 class MoeError(RuntimeError):
@@ -75,6 +77,8 @@ _SIGNATURES = [
     ("moe_route_dispatch", [_P, _I, _I, _I, _I, _I, _F, _I, _I, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P],
      _I),
     ("moe_router_route_dispatch", [_P, _I, _P, _I, _I, _I, _I, _I, _I, _F, _I, _I] + [_P] * 14, _I),
+    ("moe_route_grouped", [_P, _I, _P] + [_I] * 8 + [_F] + [_P] * 4, _I),
+    ("moe_route_grouped_dispatch", [_P, _I, _P] + [_I] * 8 + [_F] + [_P] * 10, _I),
     ("moe_ffn_workspace_bytes", [_I, _I, _I, _I], _S),
     ("moe_expert_ffn", [_P, _I, _I, _I, _P, _I, _P, _P, _P, _P, _P, _P, _I, _I, _P, _P, _S, _P], _I),
     ("moe_expert_ffn_noalloc", [_P, _I, _I, _I, _P, _I, _P, _P, _P, _P, _P, _P, _I, _I, _P, _P], _I),
@@ -289,6 +293,96 @@ def router_route_dispatch(x, w_r, k: int, mode: str, k0: int = 0, p: float = 1.0
         _ptr(route.get("n_base")), _ptr(route.get("mask")), _ptr(disp["cnt"]), _ptr(disp["offsets"]),
         _ptr(disp["perm"]), _ptr(disp["active"]), _ptr(disp["T"]), _ptr(sync), _stream(stream)))
     return logits, route, disp
+
+
+def _check_tensor(t, dtype, shape, device, name: str) -> None:
+    """A tensor the kernels index without further checks: wrong placement,
+    type, shape or layout is refused here."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a tensor, got {type(t).__name__}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, is on {t.device}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, is {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, has {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _check_device(t, name: str):
+    """The device of a call's main input: it has to be the current GPU, whose
+    current stream the call uses."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a tensor, got {type(t).__name__}")
+    dev = t.device
+    if dev.type != "cuda":
+        raise ValueError(f"{name} must be on the GPU, is on {dev}")
+    if dev.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {dev}, but the current device is cuda:{torch.cuda.current_device()}")
+    return dev
+
+
+def _grouped_args(logits, k, score, bias, n_group, topk_group, group_score, n_valid):
+    """Checks shared by the grouped-routing calls; returns (B, N, device, score, group score, topk_group)."""
+    dev = _check_device(logits, "logits")
+    if logits.dim() != 2:
+        raise ValueError(f"logits must be [B, N], has shape {tuple(logits.shape)}")
+    B, N = logits.shape
+    _check_tensor(logits, logits.dtype, (B, N), dev, "logits")
+    if bias is not None:
+        _check_tensor(bias, torch.float32, (N,), dev, "bias")
+    _check_i32_table(n_valid, 1, "n_valid", dev)
+    try:
+        sc = {"softmax": MOE_SCORE_SOFTMAX, "sigmoid": MOE_SCORE_SIGMOID}[score]
+        gs = {"max": MOE_GROUP_MAX, "top2": MOE_GROUP_TOP2}[group_score]
+    except KeyError as e:
+        raise ValueError(f"unknown score or group_score {e}") from None
+    return B, N, dev, sc, gs, n_group if topk_group is None else int(topk_group)
+
+
+def route_grouped(logits, k: int, score: str = "sigmoid", bias=None, n_group: int = 1,
+                  topk_group: int | None = None, group_score: str = "top2", renorm: bool = True,
+                  scale: float = 1.0, n_valid=None, idx=None, w=None, stream=None):
+    """Grouped routing (moe_route_grouped): scores "softmax" or "sigmoid", an
+    fp32 bias [N] that moves the choice but not the weights, the topk_group
+    best of n_group groups ranked by "max" or "top2", the k best experts in
+    them.  logits [B, N] fp32 or bf16.  Returns (idx, w), both [B, k]."""
+    B, N, dev, sc, gs, tg = _grouped_args(logits, k, score, bias, n_group, topk_group, group_score, n_valid)
+    idx = torch.empty(B, k, device=dev, dtype=torch.int32) if idx is None else idx
+    w = torch.empty(B, k, device=dev, dtype=torch.float32) if w is None else w
+    _check_tensor(idx, torch.int32, (B, k), dev, "idx")
+    _check_tensor(w, torch.float32, (B, k), dev, "w")
+    _check("moe_route_grouped", lib().moe_route_grouped(
+        _ptr(logits), _x_dtype(logits), _ptr(bias), B, N, k, sc, n_group, tg, gs, int(bool(renorm)), float(scale),
+        _ptr(n_valid), _ptr(idx), _ptr(w), _stream(stream)))
+    return idx, w
+
+
+def route_grouped_dispatch(logits, k: int, score: str = "sigmoid", bias=None, n_group: int = 1,
+                           topk_group: int | None = None, group_score: str = "top2", renorm: bool = True,
+                           scale: float = 1.0, n_valid=None, route=None, disp=None, sync=None, stream=None):
+    """Grouped routing followed by dispatch (moe_route_grouped_dispatch).
+    sync: device int32 [1] that starts at zero (allocated here if None).
+    Returns (route, disp) dicts as route_dispatch does."""
+    B, N, dev, sc, gs, tg = _grouped_args(logits, k, score, bias, n_group, topk_group, group_score, n_valid)
+    i32 = dict(device=dev, dtype=torch.int32)
+    if route is None:
+        route = dict(idx=torch.empty(B, k, **i32), w=torch.empty(B, k, device=dev, dtype=torch.float32))
+    if disp is None:
+        disp = dict(cnt=torch.empty(N, **i32), offsets=torch.empty(N + 1, **i32), perm=torch.empty(B * k, **i32),
+                    active=torch.empty(N, **i32), T=torch.empty(1, **i32))
+    sync = torch.zeros(1, **i32) if sync is None else sync
+    _check_tensor(route["idx"], torch.int32, (B, k), dev, "idx")
+    _check_tensor(route["w"], torch.float32, (B, k), dev, "w")
+    for name, n in (("cnt", N), ("offsets", N + 1), ("perm", B * k), ("active", N), ("T", 1)):
+        _check_tensor(disp[name], torch.int32, (n,), dev, name)
+    _check_i32_table(sync, 1, "sync", dev)
+    _check("moe_route_grouped_dispatch", lib().moe_route_grouped_dispatch(
+        _ptr(logits), _x_dtype(logits), _ptr(bias), B, N, k, sc, n_group, tg, gs, int(bool(renorm)), float(scale),
+        _ptr(n_valid), _ptr(route["idx"]), _ptr(route["w"]), _ptr(disp["cnt"]), _ptr(disp["offsets"]),
+        _ptr(disp["perm"]), _ptr(disp["active"]), _ptr(disp["T"]), _ptr(sync), _stream(stream)))
+    return route, disp
 
 
 def ffn_workspace_bytes(B: int, k: int, H: int, I: int) -> int:

@@ -154,6 +154,71 @@ MOE_API int moe_router_route_dispatch(const void* x, int x_dtype, const float* w
                       "moe_router_route_dispatch");
 }
 
+namespace {
+
+// Checks shared by both grouped-routing entry points.
+int check_grouped(const moe::GroupedArgs& a, int score, int group_score, int max_n, int max_k, int max_b) {
+    if (!a.logits || !a.idx || !a.w) return fail(MOE_EINVAL, "null pointer");
+    if (a.logits_dtype != MOE_DT_F32 && a.logits_dtype != MOE_DT_BF16) return fail(MOE_EINVAL, "bad logits_dtype");
+    if (reinterpret_cast<uintptr_t>(a.logits) % (a.logits_dtype == MOE_DT_F32 ? 4 : 2) != 0)
+        return fail(MOE_EINVAL, "logits must be aligned to their element size");
+    if (a.N < 1) return fail(MOE_EINVAL, "N must be >= 1");
+    if (a.N > max_n) return fail(MOE_EUNSUPPORTED, "N above the limit of this entry point");
+    if (a.k < 1 || a.k > a.N) return fail(MOE_EINVAL, "k must be in [1, N]");
+    if (a.k > max_k) return fail(MOE_EUNSUPPORTED, "k above the limit of this entry point");
+    if (a.B < 1) return fail(MOE_EINVAL, "B must be >= 1");
+    if (a.B > max_b) return fail(MOE_EUNSUPPORTED, "B above the limit of this entry point");
+    if (score != MOE_SCORE_SOFTMAX && score != MOE_SCORE_SIGMOID) return fail(MOE_EINVAL, "bad score function");
+    if (group_score != MOE_GROUP_MAX && group_score != MOE_GROUP_TOP2) return fail(MOE_EINVAL, "bad group score");
+    if (a.n_group < 1 || a.N % a.n_group) return fail(MOE_EINVAL, "n_group must divide N");
+    if (a.n_group > moe::kMaxGroups) return fail(MOE_EUNSUPPORTED, "more than 64 groups are not supported");
+    if (a.topk_group < 1 || a.topk_group > a.n_group) return fail(MOE_EINVAL, "topk_group must be in [1, n_group]");
+    if (a.k > a.topk_group * (a.N / a.n_group)) return fail(MOE_EINVAL, "k exceeds the experts of topk_group groups");
+    if (!(a.scale - a.scale == 0.0f)) return fail(MOE_EINVAL, "scale must be finite");
+    return MOE_OK;
+}
+
+moe::GroupedArgs grouped_args(const void* logits, int logits_dtype, const float* bias, int B, int N, int k, int score,
+                              int n_group, int topk_group, int group_score, int renorm, float scale,
+                              const int32_t* n_valid, int32_t* idx, float* w) {
+    moe::GroupedArgs a{};
+    a.logits = logits; a.logits_dtype = logits_dtype; a.bias = bias;
+    a.B = B; a.N = N; a.k = k;
+    a.softmax = score == MOE_SCORE_SOFTMAX;
+    a.n_group = n_group; a.topk_group = topk_group; a.group_top2 = group_score == MOE_GROUP_TOP2;
+    a.renorm = renorm != 0; a.scale = scale;
+    a.n_valid = n_valid; a.idx = idx; a.w = w;
+    return a;
+}
+
+}  // namespace
+
+MOE_API int moe_route_grouped(const void* logits, int logits_dtype, const float* bias, int B, int N, int k, int score,
+                              int n_group, int topk_group, int group_score, int renorm, float scale,
+                              const int32_t* n_valid, int32_t* idx, float* w, void* stream) {
+    const moe::GroupedArgs a = grouped_args(logits, logits_dtype, bias, B, N, k, score, n_group, topk_group,
+                                            group_score, renorm, scale, n_valid, idx, w);
+    int st = check_grouped(a, score, group_score, moe::kMaxGroupedExperts, moe::kMaxGroupedTopK, moe::kMaxTokens);
+    if (st) return st;
+    return hip_status(moe::launch_route_grouped(a, as_stream(stream)), "moe_route_grouped");
+}
+
+MOE_API int moe_route_grouped_dispatch(const void* logits, int logits_dtype, const float* bias, int B, int N, int k,
+                                       int score, int n_group, int topk_group, int group_score, int renorm,
+                                       float scale, const int32_t* n_valid, int32_t* idx, float* w, int32_t* cnt,
+                                       int32_t* offsets, int32_t* perm, int32_t* active, int32_t* T, int32_t* sync,
+                                       void* stream) {
+    moe::GroupedArgs a = grouped_args(logits, logits_dtype, bias, B, N, k, score, n_group, topk_group, group_score,
+                                      renorm, scale, n_valid, idx, w);
+    if (!cnt || !offsets || !perm || !active || !T || !sync) return fail(MOE_EINVAL, "null pointer");
+    int st = check_grouped(a, score, group_score, moe::kMaxExperts, moe::kMaxTopK, moe::kMaxBatch);
+    if (st) return st;
+    a.cnt = cnt; a.offsets = offsets; a.perm = perm; a.active = active; a.T = T; a.sync = sync;
+    hipError_t e = moe::launch_route_grouped(a, as_stream(stream));
+    if (e == hipSuccess) e = moe::launch_dispatch(idx, B, N, k, cnt, offsets, perm, active, T, as_stream(stream));
+    return hip_status(e, "moe_route_grouped_dispatch");
+}
+
 MOE_API size_t moe_ffn_workspace_bytes(int B, int k, int H, int I) {
     if (B < 1 || k < 1 || H < 1 || I < 1) return 0;
     return moe::ffn_workspace_bytes(B, k, H, I);

@@ -11,6 +11,11 @@ namespace moe {
 constexpr int kMaxExperts = 128;
 constexpr int kMaxTopK = 16;
 constexpr int kMaxBatch = 128;
+// grouped routing on its own (its dispatching form keeps the limits above)
+constexpr int kMaxGroupedExperts = 512;
+constexpr int kMaxGroupedTopK = 32;
+constexpr int kMaxGroups = 64;
+constexpr int kMaxTokens = 1 << 20;   // grouped routing, projections and the shared expert
 
 #ifdef __HIPCC__
 // Inclusive prefix sum over the 64 lanes of a wavefront (all lanes active),
@@ -97,6 +102,20 @@ hipError_t launch_expert_ffn(const FfnArgs& a, void* ws, hipStream_t s, hipEvent
 hipError_t ffn_noalloc_workspace(void** out);   // this device's static workspace
 hipError_t launch_stream_read(const void* buf, size_t bytes, int waves_per_cu, uint32_t* out, int cus,
                               hipStream_t s);
+// Grouped routing (moe_route_grouped); with perm != null the batch is also
+// dispatched.
+struct GroupedArgs {
+    const void* logits;
+    int logits_dtype;
+    const float* bias;      // null: none
+    int B, N, k, softmax, n_group, topk_group, group_top2, renorm;
+    float scale;
+    const int32_t* n_valid;
+    int32_t* idx;
+    float* w;
+    int32_t *cnt, *offsets, *perm, *active, *T, *sync;
+};
+hipError_t launch_route_grouped(const GroupedArgs& a, hipStream_t s);
 int device_cus();   // compute units of the current device (cached per device)
 
 }  // namespace moe

@@ -12,8 +12,9 @@
  *   - Results that size later work (T, counts, offsets) stay in device memory;
  *     no call reads them back to the host.
  *   - The caller owns every buffer.  Buffers must not overlap unless stated.
- *   - Limits: 1 <= N <= 128 experts, 1 <= k <= min(N, 16), 1 <= B <= 128.
- *   - Non-finite logits, and idx entries outside [-1, N) or repeated within a
+ *   - Limits: 1 <= N <= 128 experts, 1 <= k <= min(N, 16), 1 <= B <= 128;
+ *     grouped routing, the projections and the shared expert state their own.
+ *   - Non-finite logits (except in grouped routing), and idx entries outside [-1, N) or repeated within a
  *     token's row, are undefined behaviour (not checked on the device).
  *
  * Page citations
@@ -212,6 +213,46 @@ int moe_router_route_dispatch(const void *x, int x_dtype, const float *w_r, int 
                               const int32_t *k0_by_batch, float *logits, int32_t *idx, float *w,
                               int32_t *n_base, uint32_t *sbase_mask, int32_t *cnt, int32_t *offsets,
                               int32_t *perm, int32_t *active, int32_t *T, int32_t *sync, void *stream);
+
+/*
+ * Grouped routing: softmax or sigmoid scores, a per-expert balance bias,
+ * groups of experts, top-k inside the best groups.
+ *   s_e = softmax of the token's logits (MOE_SCORE_SOFTMAX) or
+ *         1 / (1 + exp(-l_e)) (MOE_SCORE_SIGMOID)
+ *   c_e = s_e + bias[e]: the value that chooses.  bias NULL: experts are
+ *         ranked by their logit (the same order).
+ *   Group g holds experts g N/n_group .. ; its value is its largest c
+ *   (MOE_GROUP_MAX) or the sum of its two largest (MOE_GROUP_TOP2; without a
+ *   bias the scores are added; a group with one selectable expert counts that
+ *   one).  The topk_group best groups stay, the k best experts in them are
+ *   taken; w = s_e (without the bias), divided by the sum over the kept
+ *   experts when renorm != 0 (all 0 if that sum is 0), times scale.  Ties go
+ *   to the lower index.  Scores, selection values and sums are formed in 64
+ *   bits and w is rounded once.
+ *   Masked experts: a NaN or -inf logit, or a NaN or -inf bias, keeps an
+ *   expert from being picked (a masked logit adds nothing to the softmax);
+ *   +inf counts as the largest float.  A token with fewer than k selectable
+ *   experts gets idx -1 and w 0 in its last slots.
+ *   logits  : [B, N] fp32 or bf16 (logits_dtype); bias : [N] fp32 or NULL
+ *   idx, w  : [B, k], best first
+ *   n_valid : NULL, or a device int32: tokens i >= *n_valid get idx -1, w 0
+ * Limits of moe_route_grouped: N <= 512, k <= 32, n_group <= 64, B <= 2^20.
+ */
+enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 };
+enum { MOE_GROUP_MAX = 0, MOE_GROUP_TOP2 = 1 };
+int moe_route_grouped(const void *logits, int logits_dtype, const float *bias, int B, int N, int k, int score,
+                      int n_group, int topk_group, int group_score, int renorm, float scale,
+                      const int32_t *n_valid, int32_t *idx, float *w, void *stream);
+
+/*
+ * moe_route_grouped followed by moe_dispatch on its idx, for the expert FFN
+ * (N <= 128, k <= 16, B <= 128).  sync: a device int32 [1], zero before the
+ * first call and left at zero by every call (calls sharing it must be ordered).
+ */
+int moe_route_grouped_dispatch(const void *logits, int logits_dtype, const float *bias, int B, int N, int k,
+                               int score, int n_group, int topk_group, int group_score, int renorm, float scale,
+                               const int32_t *n_valid, int32_t *idx, float *w, int32_t *cnt, int32_t *offsets,
+                               int32_t *perm, int32_t *active, int32_t *T, int32_t *sync, void *stream);
 
 /* Workspace bytes moe_expert_ffn needs for these sizes (host call):
  * B*k*(I + H)*4 (per routed pair, its SwiGLU activations and weighted down
