@@ -45,6 +45,16 @@ HANDLE_BYTES = ctypes.sizeof(ExpertHandle)
 assert HANDLE_BYTES == 64
 
 
+class LoraHandle(ctypes.Structure):
+    """Mirror of moe_lora_handle (32 bytes)."""
+    _fields_ = [("rank", ctypes.c_int32), ("scale", ctypes.c_float), ("a", ctypes.c_void_p), ("b", ctypes.c_void_p),
+                ("reserved", ctypes.c_int64)]
+
+
+LORA_HANDLE_BYTES = ctypes.sizeof(LoraHandle)
+assert LORA_HANDLE_BYTES == 32
+
+
 class ResidencyConfig(ctypes.Structure):
     """Mirror of moe_residency_config (include/moe_residency.h)."""
     _fields_ = [("N", ctypes.c_int), ("H", ctypes.c_int), ("I", ctypes.c_int),
@@ -82,6 +92,13 @@ _SIGNATURES = [
     ("moe_ffn_workspace_bytes", [_I, _I, _I, _I], _S),
     ("moe_expert_ffn", [_P, _I, _I, _I, _P, _I, _P, _P, _P, _P, _P, _P, _I, _I, _P, _P, _S, _P], _I),
     ("moe_expert_ffn_noalloc", [_P, _I, _I, _I, _P, _I, _P, _P, _P, _P, _P, _P, _I, _I, _P, _P], _I),
+    ("moe_lora_pack", [_P, _P, _I, _I, _I, _P, _P, _P], _I),
+    ("moe_lora_publish", [_P, _I, ctypes.POINTER(LoraHandle), _P], _I),
+    ("moe_lora_workspace_bytes", [_I] * 6, _S),
+    ("moe_lora_linear", [_P, _P, _I, _I, _P, _P, _I, _I, _I, _I, _P, _P, _I, _I, _P, _S, _P], _I),
+    ("moe_shared_ffn_workspace_bytes", [_I] * 6, _S),
+    ("moe_shared_ffn", [ctypes.POINTER(ExpertHandle), _P, _P, _P, _I, _I, _P, _P, _I, _I, _I, _I, _P, _P, _I, _I, _P,
+                        _S, _P], _I),
     ("moe_handle_publish", [_P, _I, ctypes.POINTER(ExpertHandle), _P], _I),
     ("moe_quantize_int4_g128", [_P, _I, _I, _P, _P, _P], _I),
     ("moe_pack_weights", [_I, _P, _P, _I, _I, _P, _P, _P], _I),
@@ -323,6 +340,18 @@ def _check_device(t, name: str):
     return dev
 
 
+def _scratch(stream, *shape, device, dtype, zero: bool = False):
+    """A tensor that work on `stream` uses: allocated (and cleared) in that
+    stream's order, so that its memory is not reused before that work is done."""
+    new = torch.zeros if zero else torch.empty
+    if stream is None:
+        return new(*shape, device=device, dtype=dtype)
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=device) if stream else torch.cuda.default_stream(device)
+    with torch.cuda.stream(stream):
+        return new(*shape, device=device, dtype=dtype)
+
+
 def _grouped_args(logits, k, score, bias, n_group, topk_group, group_score, n_valid):
     """Checks shared by the grouped-routing calls; returns (B, N, device, score, group score, topk_group)."""
     dev = _check_device(logits, "logits")
@@ -349,8 +378,8 @@ def route_grouped(logits, k: int, score: str = "sigmoid", bias=None, n_group: in
     best of n_group groups ranked by "max" or "top2", the k best experts in
     them.  logits [B, N] fp32 or bf16.  Returns (idx, w), both [B, k]."""
     B, N, dev, sc, gs, tg = _grouped_args(logits, k, score, bias, n_group, topk_group, group_score, n_valid)
-    idx = torch.empty(B, k, device=dev, dtype=torch.int32) if idx is None else idx
-    w = torch.empty(B, k, device=dev, dtype=torch.float32) if w is None else w
+    idx = _scratch(stream, B, k, device=dev, dtype=torch.int32) if idx is None else idx
+    w = _scratch(stream, B, k, device=dev, dtype=torch.float32) if w is None else w
     _check_tensor(idx, torch.int32, (B, k), dev, "idx")
     _check_tensor(w, torch.float32, (B, k), dev, "w")
     _check("moe_route_grouped", lib().moe_route_grouped(
@@ -368,11 +397,11 @@ def route_grouped_dispatch(logits, k: int, score: str = "sigmoid", bias=None, n_
     B, N, dev, sc, gs, tg = _grouped_args(logits, k, score, bias, n_group, topk_group, group_score, n_valid)
     i32 = dict(device=dev, dtype=torch.int32)
     if route is None:
-        route = dict(idx=torch.empty(B, k, **i32), w=torch.empty(B, k, device=dev, dtype=torch.float32))
+        route = dict(idx=_scratch(stream, B, k, **i32), w=_scratch(stream, B, k, device=dev, dtype=torch.float32))
     if disp is None:
-        disp = dict(cnt=torch.empty(N, **i32), offsets=torch.empty(N + 1, **i32), perm=torch.empty(B * k, **i32),
-                    active=torch.empty(N, **i32), T=torch.empty(1, **i32))
-    sync = torch.zeros(1, **i32) if sync is None else sync
+        disp = {name: _scratch(stream, n, **i32)
+                for name, n in (("cnt", N), ("offsets", N + 1), ("perm", B * k), ("active", N), ("T", 1))}
+    sync = _scratch(stream, 1, **i32, zero=True) if sync is None else sync
     _check_tensor(route["idx"], torch.int32, (B, k), dev, "idx")
     _check_tensor(route["w"], torch.float32, (B, k), dev, "w")
     for name, n in (("cnt", N), ("offsets", N + 1), ("perm", B * k), ("active", N), ("T", 1)):
@@ -413,6 +442,133 @@ def expert_ffn_noalloc(table, N: int, H: int, I: int, x, idx, w, disp, y, stream
     _check("moe_expert_ffn_noalloc", lib().moe_expert_ffn_noalloc(
         _ptr(table), N, H, I, _ptr(x), _x_dtype(x), _ptr(idx), _ptr(w), _ptr(disp["offsets"]),
         _ptr(disp["perm"]), _ptr(disp["active"]), _ptr(disp["T"]), B, k, _ptr(y), _stream(stream)))
+    return y
+
+
+def lora_pack(a, b, stream=None):
+    """Pack one adapter's A [rank, H] and B [O, rank] (bf16, row-major) for
+    the kernels; returns (packed A, packed B, padded rank)."""
+    dev = _check_device(a, "A")
+    if a.dim() != 2 or not isinstance(b, torch.Tensor) or b.dim() != 2:
+        raise ValueError("A must be [rank, H] and B [O, rank]")
+    (rank, H), O = a.shape, b.shape[0]
+    _check_tensor(a, torch.bfloat16, (rank, H), dev, "A")
+    _check_tensor(b, torch.bfloat16, (O, rank), dev, "B")
+    R = (rank + 15) // 16 * 16
+    dst_a = _scratch(stream, R, H, device=dev, dtype=torch.bfloat16)
+    dst_b = _scratch(stream, O, R, device=dev, dtype=torch.bfloat16)
+    _check("moe_lora_pack", lib().moe_lora_pack(_ptr(a), _ptr(b), rank, H, O, _ptr(dst_a), _ptr(dst_b),
+                                                _stream(stream)))
+    return dst_a, dst_b, R
+
+
+def lora_publish(table, i: int, h: LoraHandle, stream=None):
+    """Publish adapter i's handle in a device table (uint8, 32 bytes per adapter)."""
+    dev = _check_device(table, "table")
+    _check_tensor(table, torch.uint8, (table.numel(),), dev, "table")
+    if not 0 <= i < table.numel() // LORA_HANDLE_BYTES:
+        raise ValueError(f"adapter {i} is outside the table")
+    _check("moe_lora_publish", lib().moe_lora_publish(_ptr(table), i, ctypes.byref(h), _stream(stream)))
+
+
+def _dt(dtype) -> int:
+    if dtype == torch.bfloat16:
+        return MOE_DT_BF16
+    if dtype == torch.float32:
+        return MOE_DT_F32
+    raise TypeError(f"must be float32 or bfloat16, got {dtype}")
+
+
+def lora_workspace_bytes(B: int, H: int, O: int, max_rank: int, x_dtype, y_dtype) -> int:
+    return int(lib().moe_lora_workspace_bytes(B, H, O, max_rank, _dt(x_dtype), _dt(y_dtype)))
+
+
+def shared_ffn_workspace_bytes(B: int, H: int, I: int, max_rank: int, x_dtype, y_dtype) -> int:
+    return int(lib().moe_shared_ffn_workspace_bytes(B, H, I, max_rank, _dt(x_dtype), _dt(y_dtype)))
+
+
+def _proj_args(x, y, y_dtype, O, adapter, tables, n_valid, ws, ws_bytes, accumulate, stream):
+    """Checks shared by lora_linear and shared_ffn.  tables: (LoraTable or
+    None, H, O) for each projection.  Returns (B, H, y, ws, n_adapters, max_rank)."""
+    dev = _check_device(x, "x")
+    if x.dim() != 2:
+        raise ValueError(f"x must be [B, H], has shape {tuple(x.shape)}")
+    B, H = x.shape
+    _x_dtype(x)
+    _check_tensor(x, x.dtype, (B, H), dev, "x")
+    if y is None:
+        if accumulate:
+            raise ValueError("accumulating needs the y to add to")
+        y = _scratch(stream, B, O, device=dev, dtype=x.dtype if y_dtype is None else y_dtype)
+    _dt(y.dtype)
+    _check_tensor(y, y.dtype if y_dtype is None else y_dtype, (B, O), dev, "y")
+    _check_i32_table(n_valid, 1, "n_valid", dev)
+    used = [(t, h, o) for t, h, o in tables if t is not None]
+    n = rank = 0
+    if used:
+        n, rank = used[0][0].n, max(t.max_rank for t, _, _ in used)
+        for t, h, o in used:
+            if (t.H, t.O) != (h, o):
+                raise ValueError(f"an adapter table of a [{t.O}, {t.H}] projection beside one of [{o}, {h}]")
+            if t.n != n:
+                raise ValueError("the adapter tables of one call must have the same number of entries")
+            _check_tensor(t.handles, torch.uint8, (n * LORA_HANDLE_BYTES,), dev, "adapter table")
+        if adapter is None:
+            raise ValueError("adapter tables need the tokens' adapter ids")
+        _check_tensor(adapter, torch.int32, (B,), dev, "adapter")
+    need = ws_bytes(B, H, rank, x.dtype, y.dtype)
+    if ws is None and need:
+        ws = _scratch(stream, need, device=dev, dtype=torch.uint8)
+    if ws is not None and (ws.device != dev or not ws.is_contiguous()):
+        raise ValueError(f"ws must be contiguous on {dev}")
+    return B, H, y, ws, n, rank
+
+
+def lora_linear(x, w, lora=None, adapter=None, y=None, y_dtype=None, accumulate: bool = False, n_valid=None, ws=None,
+                stream=None):
+    """y = x W^T plus every token's own adapter (moe_lora_linear).
+
+    x [B, H] fp32 or bf16; w the packed bf16 [O, H] matrix (pack_weights);
+    lora a LoraTable and adapter the tokens' int32 ids [B] (outside the table:
+    none), or both None; y [B, O] fp32 or bf16 (allocated in x's type, or
+    y_dtype, if None); accumulate adds to an fp32 y; rows at or past n_valid
+    (device int32 [1]) are left as they are.
+    """
+    O = w.shape[0]
+    B, H, y, ws, n, rank = _proj_args(x, y, y_dtype, O, adapter, [(lora, x.shape[-1], O)], n_valid, ws,
+                                      lambda B, H, r, xd, yd: lora_workspace_bytes(B, H, O, r, xd, yd), accumulate, stream)
+    _check_tensor(w, torch.bfloat16, (O, H), x.device, "w")
+    _check("moe_lora_linear", lib().moe_lora_linear(
+        _ptr(w), None if lora is None else _ptr(lora.handles), n, rank, None if lora is None else _ptr(adapter),
+        _ptr(x), _x_dtype(x), B, H, O, _ptr(n_valid), _ptr(y), _dt(y.dtype), int(bool(accumulate)), _ptr(ws),
+        0 if ws is None else ws.numel() * ws.element_size(), _stream(stream)))
+    return y
+
+
+def shared_ffn(x, shared, loras=None, adapter=None, y=None, y_dtype=None, accumulate: bool = False, n_valid=None,
+               ws=None, stream=None):
+    """The shared expert (moe_shared_ffn): shared is an ExpertTensors of format
+    MOE_W_BF16; loras three LoraTables (gate, up, down), any of them None.
+    Otherwise as lora_linear."""
+    if shared.fmt != MOE_W_BF16:
+        raise ValueError("the shared expert's weights must be bf16")
+    I, H = shared.gate.shape
+    loras = (None, None, None) if loras is None else tuple(loras)
+    if len(loras) != 3:
+        raise ValueError("loras must be three tables (gate, up, down)")
+    B, Hx, y, ws, n, rank = _proj_args(x, y, y_dtype, H, adapter,
+                                       [(loras[0], H, I), (loras[1], H, I), (loras[2], I, H)], n_valid, ws,
+                                       lambda B, H, r, xd, yd: shared_ffn_workspace_bytes(B, H, I, r, xd, yd),
+                                       accumulate, stream)
+    if Hx != H:
+        raise ValueError(f"x has {Hx} columns, the shared expert {H}")
+    for name, t, shape in (("gate", shared.gate, (I, H)), ("up", shared.up, (I, H)), ("down", shared.down, (H, I))):
+        _check_tensor(t, torch.bfloat16, shape, x.device, name)
+    h = shared.handle()
+    _check("moe_shared_ffn", lib().moe_shared_ffn(
+        ctypes.byref(h), *[None if t is None else _ptr(t.handles) for t in loras], n, rank,
+        None if rank == 0 else _ptr(adapter), _ptr(x), _x_dtype(x), B, H, I, _ptr(n_valid), _ptr(y), _dt(y.dtype),
+        int(bool(accumulate)), _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(), _stream(stream)))
     return y
 
 

@@ -285,6 +285,129 @@ MOE_API int moe_expert_ffn_noalloc(const moe_expert_handle* table, int N, int H,
     return hip_status(moe::launch_expert_ffn(a, ws, as_stream(stream)), "moe_expert_ffn_noalloc");
 }
 
+namespace {
+
+bool misaligned(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a != 0; }
+int padded_rank(int r) { return (r + 15) / 16 * 16; }
+
+// Checks shared by moe_lora_linear and moe_shared_ffn (everything but the
+// weights, the tables and the workspace).
+int check_proj(const moe::ProjArgs& a, bool any_table) {
+    if (!a.x || !a.y) return fail(MOE_EINVAL, "null pointer");
+    if (a.x_dtype != MOE_DT_F32 && a.x_dtype != MOE_DT_BF16) return fail(MOE_EINVAL, "bad x_dtype");
+    if (a.y_dtype != MOE_DT_F32 && a.y_dtype != MOE_DT_BF16) return fail(MOE_EINVAL, "bad y_dtype");
+    if (a.accumulate && a.y_dtype != MOE_DT_F32) return fail(MOE_EINVAL, "accumulating needs an fp32 y");
+    if (a.B < 1) return fail(MOE_EINVAL, "B must be >= 1");
+    if (a.B > moe::kMaxTokens) return fail(MOE_EUNSUPPORTED, "B above 2^20 is not supported");
+    if (misaligned(a.x, 16) || misaligned(a.y, 16)) return fail(MOE_EINVAL, "x and y must be 16-byte aligned");
+    if (any_table) {
+        if (!a.adapter) return fail(MOE_EINVAL, "adapters need their token ids");
+        if (a.n_adapters < 1) return fail(MOE_EINVAL, "n_adapters must be >= 1");
+        if (a.max_rank < 16 || a.max_rank % 16) return fail(MOE_EINVAL, "max_rank must be a positive multiple of 16");
+        if (a.max_rank > moe::kMaxLoraRank) return fail(MOE_EUNSUPPORTED, "max_rank above 256 is not supported");
+    }
+    return MOE_OK;
+}
+
+int check_workspace(const void* ws, size_t have, size_t need) {
+    if (need == 0) return MOE_OK;
+    if (!ws) return fail(MOE_EINVAL, "null workspace");
+    if (have < need) return fail(MOE_EINVAL, "workspace too small");
+    if (misaligned(ws, 256)) return fail(MOE_EINVAL, "workspace must be 256-byte aligned");
+    return MOE_OK;
+}
+
+bool proj_sizes_ok(int B, int max_rank) { return B >= 1 && B <= moe::kMaxTokens && max_rank >= 0 && max_rank <= moe::kMaxLoraRank; }
+
+}  // namespace
+
+MOE_API int moe_lora_pack(const uint16_t* a, const uint16_t* b, int rank, int H, int O, void* dst_a, void* dst_b,
+                          void* stream) {
+    if (!a || !b || !dst_a || !dst_b) return fail(MOE_EINVAL, "null pointer");
+    if (rank < 1) return fail(MOE_EINVAL, "rank must be >= 1");
+    if (rank > moe::kMaxLoraRank) return fail(MOE_EUNSUPPORTED, "rank above 256 is not supported");
+    if (H < 32 || H % 32) return fail(MOE_EINVAL, "H must be a positive multiple of 32");
+    if (O < 16 || O % 16) return fail(MOE_EINVAL, "O must be a positive multiple of 16");
+    if (H > 16384 || O > 16384) return fail(MOE_EUNSUPPORTED, "H and O above 16384 are not supported");
+    if (misaligned(a, 16) || misaligned(dst_a, 16) || misaligned(dst_b, 16) || misaligned(b, 2))
+        return fail(MOE_EINVAL, "a, dst_a and dst_b must be 16-byte aligned");
+    return hip_status(moe::launch_lora_pack(a, b, rank, H, O, dst_a, dst_b, as_stream(stream)), "moe_lora_pack");
+}
+
+MOE_API int moe_lora_publish(moe_lora_handle* table, int i, const moe_lora_handle* h, void* stream) {
+    if (!table || !h) return fail(MOE_EINVAL, "null pointer");
+    if (i < 0) return fail(MOE_EINVAL, "adapter index must be >= 0");
+    if (misaligned(table, 16)) return fail(MOE_EINVAL, "handle table must be 16-byte aligned");
+    if (h->rank < 0 || h->rank % 16) return fail(MOE_EINVAL, "a handle's rank is the padded rank, a multiple of 16");
+    if (h->rank > moe::kMaxLoraRank) return fail(MOE_EUNSUPPORTED, "rank above 256 is not supported");
+    if (h->rank > 0) {
+        if (!h->a || !h->b) return fail(MOE_EINVAL, "null adapter pointer");
+        if (misaligned(h->a, 16) || misaligned(h->b, 16)) return fail(MOE_EINVAL, "packed adapters must be 16-byte aligned");
+        if (!(h->scale - h->scale == 0.0f)) return fail(MOE_EINVAL, "scale must be finite");
+    }
+    return hip_status(moe::launch_lora_publish(table, i, *h, as_stream(stream)), "moe_lora_publish");
+}
+
+MOE_API size_t moe_lora_workspace_bytes(int B, int H, int O, int max_rank, int x_dtype, int y_dtype) {
+    (void)H; (void)O; (void)x_dtype; (void)y_dtype;
+    return proj_sizes_ok(B, max_rank) ? moe::lora_workspace_bytes(B, padded_rank(max_rank)) : 0;
+}
+
+MOE_API int moe_lora_linear(const void* w, const moe_lora_handle* table, int n_adapters, int max_rank,
+                            const int32_t* adapter, const void* x, int x_dtype, int B, int H, int O,
+                            const int32_t* n_valid, void* y, int y_dtype, int accumulate, void* ws, size_t ws_bytes,
+                            void* stream) {
+    if (!w) return fail(MOE_EINVAL, "null pointer");
+    moe::ProjArgs a{};
+    a.w[0] = w; a.table[0] = table; a.adapter = table ? adapter : nullptr;
+    a.n_adapters = n_adapters; a.max_rank = table ? max_rank : 0;
+    a.x = x; a.x_dtype = x_dtype; a.B = B; a.H = H; a.O = O;
+    a.n_valid = n_valid; a.y = y; a.y_dtype = y_dtype; a.accumulate = accumulate != 0;
+    int st = check_proj(a, table != nullptr);
+    if (st) return st;
+    if (H < 32 || H % 32) return fail(MOE_EINVAL, "H must be a positive multiple of 32");
+    if (O < 16 || O % 16) return fail(MOE_EINVAL, "O must be a positive multiple of 16");
+    if (H > 16384 || O > 16384) return fail(MOE_EUNSUPPORTED, "H and O above 16384 are not supported");
+    if (misaligned(w, 16) || misaligned(table, 16)) return fail(MOE_EINVAL, "w and the handle table must be 16-byte aligned");
+    st = check_workspace(ws, ws_bytes, moe_lora_workspace_bytes(B, H, O, a.max_rank, x_dtype, y_dtype));
+    if (st) return st;
+    return hip_status(moe::launch_lora_linear(a, ws, as_stream(stream)), "moe_lora_linear");
+}
+
+MOE_API size_t moe_shared_ffn_workspace_bytes(int B, int H, int I, int max_rank, int x_dtype, int y_dtype) {
+    (void)H; (void)x_dtype;
+    return proj_sizes_ok(B, max_rank) && I >= 1 ? moe::shared_ffn_workspace_bytes(B, I, padded_rank(max_rank), y_dtype) : 0;
+}
+
+MOE_API int moe_shared_ffn(const moe_expert_handle* shared, const moe_lora_handle* t_gate,
+                           const moe_lora_handle* t_up, const moe_lora_handle* t_down, int n_adapters, int max_rank,
+                           const int32_t* adapter, const void* x, int x_dtype, int B, int H, int I,
+                           const int32_t* n_valid, void* y, int y_dtype, int accumulate, void* ws, size_t ws_bytes,
+                           void* stream) {
+    if (!shared) return fail(MOE_EINVAL, "null pointer");
+    if (shared->fmt != MOE_W_BF16) return fail(MOE_EUNSUPPORTED, "the shared expert's weights must be bf16");
+    if (!shared->w_gate || !shared->w_up || !shared->w_down) return fail(MOE_EINVAL, "null weight pointer");
+    if (misaligned(shared->w_gate, 16) || misaligned(shared->w_up, 16) || misaligned(shared->w_down, 16))
+        return fail(MOE_EINVAL, "packed weights must be 16-byte aligned");
+    const bool any = t_gate || t_up || t_down;
+    moe::ProjArgs a{};
+    a.w[0] = shared->w_gate; a.w[1] = shared->w_up;
+    a.table[0] = t_gate; a.table[1] = t_up;
+    a.adapter = any ? adapter : nullptr;
+    a.n_adapters = n_adapters; a.max_rank = any ? max_rank : 0;
+    a.x = x; a.x_dtype = x_dtype; a.B = B; a.H = H; a.O = I;
+    a.n_valid = n_valid; a.y = y; a.y_dtype = y_dtype; a.accumulate = accumulate != 0;
+    int st = check_proj(a, any);
+    if (st) return st;
+    if (H < 32 || H % 32 || I < 32 || I % 32) return fail(MOE_EINVAL, "H and I must be positive multiples of 32");
+    if (H > 16384 || I > 16384) return fail(MOE_EUNSUPPORTED, "H and I above 16384 are not supported");
+    if (misaligned(t_gate, 16) || misaligned(t_up, 16) || misaligned(t_down, 16))
+        return fail(MOE_EINVAL, "handle tables must be 16-byte aligned");
+    st = check_workspace(ws, ws_bytes, moe_shared_ffn_workspace_bytes(B, H, I, a.max_rank, x_dtype, y_dtype));
+    if (st) return st;
+    return hip_status(moe::launch_shared_ffn(a, shared->w_down, t_down, ws, as_stream(stream)), "moe_shared_ffn");
+}
+
 MOE_API int moe_handle_publish(moe_expert_handle* table, int e, const moe_expert_handle* h,
                                void* stream) {
     if (!table || !h) return fail(MOE_EINVAL, "null pointer");

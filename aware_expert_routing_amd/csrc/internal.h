@@ -116,6 +116,30 @@ struct GroupedArgs {
     int32_t *cnt, *offsets, *perm, *active, *T, *sync;
 };
 hipError_t launch_route_grouped(const GroupedArgs& a, hipStream_t s);
+
+// One projection with adapters (or the gate/up pair: two matrices, tables and
+// v).  H input columns, O output rows.
+constexpr int kMaxLoraRank = 256;
+struct ProjArgs {
+    const void* w[2];
+    const moe_lora_handle* table[2];   // null: no adapters on that matrix
+    const int32_t* adapter;            // null: none
+    int n_adapters, max_rank;
+    const void* x;
+    int x_dtype, B, H, O;
+    const int32_t* n_valid;
+    void* y;
+    int y_dtype, accumulate;
+    float* v[2];                       // [B, max_rank]: scale A x
+};
+size_t lora_workspace_bytes(int B, int max_rank);
+size_t shared_ffn_workspace_bytes(int B, int I, int max_rank, int y_dtype);
+hipError_t launch_lora_linear(ProjArgs a, void* ws, hipStream_t s);
+hipError_t launch_shared_ffn(ProjArgs gate_up, const void* w_down, const moe_lora_handle* t_down, void* ws,
+                             hipStream_t s);
+hipError_t launch_lora_pack(const uint16_t* a, const uint16_t* b, int rank, int H, int O, void* dst_a, void* dst_b,
+                            hipStream_t s);
+hipError_t launch_lora_publish(moe_lora_handle* table, int i, moe_lora_handle h, hipStream_t s);
 int device_cus();   // compute units of the current device (cached per device)
 
 }  // namespace moe

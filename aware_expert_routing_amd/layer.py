@@ -48,6 +48,18 @@ class ExpertTensors:
 
 
 @dataclass
+class GroupedRouting:
+    """A layer's grouped router (moe_route_grouped): the arguments of route_grouped."""
+    score: str = "sigmoid"
+    bias: torch.Tensor | None = None
+    n_group: int = 1
+    topk_group: int | None = None
+    group_score: str = "top2"
+    renorm: bool = True
+    scale: float = 1.0
+
+
+@dataclass
 class Buffers:
     """Per-batch-size device buffers for one forward call.
 
@@ -56,7 +68,8 @@ class Buffers:
     vanilla top-k leaves them as they were), T [1] (the same tensor as
     disp["T"]).  disp: cnt, offsets, perm, active, T (dispatch output).
     y: [B, H] layer output.  ws: the expert FFN's workspace.  extra["sync"]:
-    the fused router kernel's completion counter (zero between calls)."""
+    the fused router kernel's completion counter (zero between calls);
+    extra["shared_ws"]: the shared expert's workspace."""
     B: int
     logits: torch.Tensor
     route: dict
@@ -68,7 +81,14 @@ class Buffers:
 
 class MoELayer:
     def __init__(self, H: int, I: int, N: int, k: int, w_r: torch.Tensor | None,
-                 experts: list[ExpertTensors], device="cuda"):
+                 experts: list[ExpertTensors], device="cuda", grouped: GroupedRouting | None = None,
+                 shared: ExpertTensors | None = None, loras=None):
+        """grouped: the router of mode "grouped".  shared: a shared expert
+        (bf16) whose output every forward call adds to y; loras: its three
+        LoraTables (gate, up, down), read with the adapter ids of the call."""
+        if loras is not None and shared is None:
+            raise ValueError("adapters need the shared expert whose projections they adapt")
+        self.grouped, self.shared, self.loras = grouped, shared, None if loras is None else tuple(loras)
         self.H, self.I, self.N, self.k = H, I, N, k
         self.w_r = w_r
         self.experts = list(experts)
@@ -97,17 +117,30 @@ class MoELayer:
             b = Buffers(B, torch.empty(B, N, device=dev, dtype=torch.float32), route, disp,
                         torch.empty(B, self.H, device=dev, dtype=torch.float32), ws,
                         {"sync": torch.zeros(1, **i32)})
+            if self.shared is not None:
+                rank = max((t.max_rank for t in self.loras or () if t is not None), default=0)
+                need = max(L.shared_ffn_workspace_bytes(B, self.H, self.shared.gate.shape[0], rank, xd, torch.float32)
+                           for xd in (torch.float32, torch.bfloat16))
+                b.extra["shared_ws"] = torch.empty(need, device=dev, dtype=torch.uint8)
             self._bufs[B] = b
         return b
 
     def route(self, logits: torch.Tensor, mode: str, k0: int = 0, p: float = 1.0,
               buf: Buffers | None = None, stream=None, max_p: int | None = None, n_valid=None,
               k0_by_batch=None) -> Buffers:
-        """Routing ("topk", "oea" or "pruned") and dispatch (one launch up to 48 tokens); n_valid
+        """Routing ("topk", "oea", "pruned" or "grouped") and dispatch (one launch up to 48 tokens); n_valid
         (device int32 [1]) marks trailing tokens as padding; k0_by_batch (device
-        int32 [B+1], see k0_schedule) picks k0 from the real batch size."""
+        int32 [B+1], see k0_schedule) picks k0 from the real batch size (OEA
+        and pruned; mode "grouped" takes none of k0, p, max_p)."""
         B = logits.shape[0]
         buf = buf or self.buffers(B)
+        if mode == "grouped":
+            g = self.grouped
+            if g is None:
+                raise ValueError('mode "grouped" needs a layer built with a GroupedRouting')
+            L.route_grouped_dispatch(logits, self.k, g.score, g.bias, g.n_group, g.topk_group, g.group_score, g.renorm,
+                                     g.scale, n_valid, buf.route, buf.disp, buf.extra["sync"], stream)
+            return buf
         if mode not in ("topk", "oea", "pruned"):
             raise ValueError(mode)
         L.route_dispatch(logits, self.k, mode, k0, p, True, buf.route, buf.disp, stream, max_p, n_valid,
@@ -118,16 +151,31 @@ class MoELayer:
         return L.expert_ffn(self.table, self.N, self.H, self.I, x, buf.route["idx"], buf.route["w"],
                             buf.disp, buf.y, buf.ws, stream)
 
+    def shared_ffn(self, x: torch.Tensor, buf: Buffers, adapter=None, n_valid=None, stream=None) -> torch.Tensor:
+        """The shared expert of every (real) token, added to buf.y; adapter
+        (device int32 [B]) names each token's adapter, None or an entry outside
+        the tables none."""
+        return L.shared_ffn(x, self.shared, None if adapter is None else self.loras, adapter, buf.y, None, True,
+                            n_valid, buf.extra["shared_ws"], stream)
+
     def forward(self, x: torch.Tensor, mode: str = "oea", k0: int = 3, p: float = 1.0,
                 logits: torch.Tensor | None = None, stream=None, max_p: int | None = None,
-                n_valid=None, k0_by_batch=None) -> Buffers:
+                n_valid=None, k0_by_batch=None, adapter=None) -> Buffers:
         """Whole layer.  If `logits` is given the router GEMV is skipped;
         otherwise router, routing and dispatch run together (one launch up to 48
-        tokens)."""
+        tokens; mode "grouped" takes one for the logits).  A layer with a
+        shared expert then adds its output, through the adapters `adapter`
+        names."""
+        if adapter is not None and self.loras is None:
+            raise ValueError("the layer has no adapter tables")
         B = x.shape[0]
         buf = self.buffers(B)
         stream = L._stream(stream)   # looked up once for both calls
-        if logits is None:
+        if mode == "grouped":
+            if logits is None:
+                logits = L.router_logits(x, self.w_r, buf.logits, stream)
+            self.route(logits, mode, buf=buf, stream=stream, n_valid=n_valid)
+        elif logits is None:
             if mode not in ("topk", "oea", "pruned"):
                 raise ValueError(mode)
             L.router_route_dispatch(x, self.w_r, self.k, mode, k0, p, True, buf.route, buf.disp, buf.logits,
@@ -135,10 +183,12 @@ class MoELayer:
         else:
             self.route(logits, mode, k0, p, buf, stream, max_p, n_valid, k0_by_batch)
         self.ffn(x, buf, stream)
+        if self.shared is not None:
+            self.shared_ffn(x, buf, adapter, n_valid, stream)
         return buf
 
     def capture(self, x: torch.Tensor, mode: str = "oea", k0: int = 3, p: float = 1.0,
-                max_p: int | None = None, n_valid=None, k0_by_batch=None) -> torch.cuda.CUDAGraph:
+                max_p: int | None = None, n_valid=None, k0_by_batch=None, adapter=None) -> torch.cuda.CUDAGraph:
         """Capture forward(x, ...) into a HIP graph (every kernel of the layer, no
         allocation or memset inside).  Replaying it recomputes the layer for
         whatever `x` and `n_valid` hold at replay time; results land in
@@ -147,23 +197,24 @@ class MoELayer:
         side = torch.cuda.Stream()
         side.wait_stream(torch.cuda.current_stream())
         with torch.cuda.stream(side):   # warm-up outside capture (allocates the buffers)
-            self.forward(x, mode, k0, p, max_p=max_p, n_valid=n_valid, k0_by_batch=k0_by_batch)
+            self.forward(x, mode, k0, p, max_p=max_p, n_valid=n_valid, k0_by_batch=k0_by_batch, adapter=adapter)
         torch.cuda.current_stream().wait_stream(side)
         torch.cuda.synchronize()
         graph = torch.cuda.CUDAGraph()
         with torch.cuda.graph(graph):
-            self.forward(x, mode, k0, p, max_p=max_p, n_valid=n_valid, k0_by_batch=k0_by_batch)
+            self.forward(x, mode, k0, p, max_p=max_p, n_valid=n_valid, k0_by_batch=k0_by_batch, adapter=adapter)
         return graph
 
 
 def capture_layers(calls, mode: str = "oea", k0: int = 3, p: float = 1.0, max_p: int | None = None,
-                   n_valid=None, k0_by_batch=None) -> torch.cuda.CUDAGraph:
+                   n_valid=None, k0_by_batch=None, adapter=None) -> torch.cuda.CUDAGraph:
     """Capture the forward calls of several layers, in the order given, into
     one HIP graph; `calls` is a list of (MoELayer, x) pairs.  One replay runs
     them all (a decode step's MoE layers), so the fixed cost of launching a
     graph is paid once per step rather than once per layer, and the host
     spends one replay call on the whole step.  Each layer's results land in
-    its own buffers(B), as with MoELayer.capture."""
+    its own buffers(B), as with MoELayer.capture.  adapter: the batch's adapter
+    ids, the same for every layer (all of them need adapter tables)."""
     calls = list(calls)
     if not calls:
         raise ValueError("no layers to capture")
@@ -171,13 +222,13 @@ def capture_layers(calls, mode: str = "oea", k0: int = 3, p: float = 1.0, max_p:
     side.wait_stream(torch.cuda.current_stream())
     with torch.cuda.stream(side):   # warm-up outside capture (allocates every layer's buffers)
         for layer, x in calls:
-            layer.forward(x, mode, k0, p, max_p=max_p, n_valid=n_valid, k0_by_batch=k0_by_batch)
+            layer.forward(x, mode, k0, p, max_p=max_p, n_valid=n_valid, k0_by_batch=k0_by_batch, adapter=adapter)
     torch.cuda.current_stream().wait_stream(side)
     torch.cuda.synchronize()
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
         for layer, x in calls:
-            layer.forward(x, mode, k0, p, max_p=max_p, n_valid=n_valid, k0_by_batch=k0_by_batch)
+            layer.forward(x, mode, k0, p, max_p=max_p, n_valid=n_valid, k0_by_batch=k0_by_batch, adapter=adapter)
     return graph
 
 

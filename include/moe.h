@@ -325,6 +325,82 @@ int moe_expert_ffn_noalloc(const moe_expert_handle *table, int N, int H, int I, 
                            float *y, void *stream);
 
 /*
+ * Low-rank adapters of many requests beside a projection they share.
+ * An adapter is reached through a stable 32-byte handle in a device table, as
+ * expert versions are [DYN section 2.2 / 3.2]: publishing another adapter
+ * rewrites the handle and no kernel argument, so captured graphs follow it.
+ */
+typedef struct moe_lora_handle {
+    int32_t rank;            /* padded rank, a multiple of 16; 0: no adapter    */
+    float scale;             /* s in s B A x                                    */
+    const void *a;           /* packed A (moe_lora_pack), rank * H * 2 bytes    */
+    const void *b;           /* packed B, O * rank * 2 bytes                    */
+    int64_t reserved;        /* set to 0                                        */
+} moe_lora_handle;
+
+/*
+ * Pack one adapter: a [rank, H] and b [O, rank] row-major bf16 bits; the rank
+ * is padded with zeros to R = the next multiple of 16.
+ *   dst_a : R * H * 2 bytes, tiles of 16 x 32 as moe_pack_weights writes them
+ *   dst_b : O * R * 2 bytes: block (ob, rb) of 16 rows x 16 ranks is the 512
+ *           bytes at (ob * R/16 + rb) * 512, in which the 8 bytes at 8 * l
+ *           hold row l % 16, ranks 4 * (l / 16) .. + 3
+ * 1 <= rank <= 256; H a multiple of 32 and O of 16, both at most 16384; a,
+ * dst_a and dst_b 16-byte aligned, nothing overlapping.
+ */
+int moe_lora_pack(const uint16_t *a, const uint16_t *b, int rank, int H, int O, void *dst_a, void *dst_b,
+                  void *stream);
+
+/* Publish adapter i's handle (host, copied by value), ordered on `stream` as
+ * moe_handle_publish; rank 0 clears it. */
+int moe_lora_publish(moe_lora_handle *table, int i, const moe_lora_handle *h, void *stream);
+
+/*
+ * y_i = W x_i + s_a B_a (A_a x_i) for every token i, a = adapter[i].
+ *   w       : packed bf16 [O, H] (moe_pack_weights)
+ *   table   : [n_adapters] handles (16-byte aligned), or NULL: no adapters
+ *             (adapter, n_adapters and max_rank are then ignored)
+ *   adapter : [B] int32; an entry outside [0, n_adapters), or one whose handle
+ *             has rank 0, gives W x_i alone
+ *   max_rank: a multiple of 16, at least every padded rank in use: an adapter
+ *             of a larger rank is left out.  At most 256
+ *   x       : [B, H] fp32 or bf16;  y : [B, O] fp32 or bf16 (16-byte aligned)
+ *   accumulate : nonzero adds to y (fp32 only) in place of overwriting it
+ *   n_valid : NULL, or a device int32: rows i >= *n_valid of y are left as
+ *             they are and rows of x behind it are not read
+ *   ws      : moe_lora_workspace_bytes(...), 256-byte aligned (scratch; calls
+ *             that share it must be ordered).  May be NULL if that is 0.
+ * Sums are fp32.  An fp32 x enters the bf16 products as three terms that hold
+ * all of its 24 bits; A_a x_i is held in fp32 and enters the second product
+ * as three such terms for an fp32 y and as two (16 bits) for a bf16 y.
+ * H a multiple of 32, O of 16, both at most 16384; B <= 2^20.  Deterministic;
+ * a token's y does not depend on the other tokens' adapters.
+ */
+size_t moe_lora_workspace_bytes(int B, int H, int O, int max_rank, int x_dtype, int y_dtype);
+int moe_lora_linear(const void *w, const moe_lora_handle *table, int n_adapters, int max_rank,
+                    const int32_t *adapter, const void *x, int x_dtype, int B, int H, int O, const int32_t *n_valid,
+                    void *y, int y_dtype, int accumulate, void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * The shared expert, an FFN that every token passes beside its routed experts,
+ * with adapters on its three projections:
+ *   g = W_gate x + adapters, u = W_up x + adapters, h = silu(g) u,
+ *   y = W_down h + adapters  (accumulate: y += that)
+ *   shared : (host) a handle of format MOE_W_BF16, weights packed as for
+ *            moe_expert_ffn (gate, up [I, H], down [H, I])
+ *   t_gate, t_up, t_down : adapter tables of the three projections, any of
+ *            them NULL; one adapter id per token serves all three
+ * The remaining arguments and rules are those of moe_lora_linear.  h is kept
+ * in y's type: fp32 (three terms in the down projection), or rounded to bf16
+ * where y is bf16.  H and I multiples of 32, at most 16384.
+ */
+size_t moe_shared_ffn_workspace_bytes(int B, int H, int I, int max_rank, int x_dtype, int y_dtype);
+int moe_shared_ffn(const moe_expert_handle *shared, const moe_lora_handle *t_gate, const moe_lora_handle *t_up,
+                   const moe_lora_handle *t_down, int n_adapters, int max_rank, const int32_t *adapter,
+                   const void *x, int x_dtype, int B, int H, int I, const int32_t *n_valid, void *y, int y_dtype,
+                   int accumulate, void *ws, size_t ws_bytes, void *stream);
+
+/*
  * Publish a new version of expert e's handle [DYN section 2.2 / 3.2
  * "publish-then-switch": a version becomes visible only after its data is
  * complete; the forward path keeps using the previous version until then].
