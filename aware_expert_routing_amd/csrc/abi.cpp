@@ -292,11 +292,11 @@ int padded_rank(int r) { return (r + 15) / 16 * 16; }
 
 // Checks shared by moe_lora_linear and moe_shared_ffn (everything but the
 // weights, the tables and the workspace).
-int check_proj(const moe::ProjArgs& a, bool any_table) {
+int check_proj(const moe::ProjArgs& a, int x_dtype, int y_dtype, bool any_table) {
     if (!a.x || !a.y) return fail(MOE_EINVAL, "null pointer");
-    if (a.x_dtype != MOE_DT_F32 && a.x_dtype != MOE_DT_BF16) return fail(MOE_EINVAL, "bad x_dtype");
-    if (a.y_dtype != MOE_DT_F32 && a.y_dtype != MOE_DT_BF16) return fail(MOE_EINVAL, "bad y_dtype");
-    if (a.accumulate && a.y_dtype != MOE_DT_F32) return fail(MOE_EINVAL, "accumulating needs an fp32 y");
+    if (x_dtype != MOE_DT_F32 && x_dtype != MOE_DT_BF16) return fail(MOE_EINVAL, "bad x_dtype");
+    if (y_dtype != MOE_DT_F32 && y_dtype != MOE_DT_BF16) return fail(MOE_EINVAL, "bad y_dtype");
+    if (a.accumulate && y_dtype != MOE_DT_F32) return fail(MOE_EINVAL, "accumulating needs an fp32 y");
     if (a.B < 1) return fail(MOE_EINVAL, "B must be >= 1");
     if (a.B > moe::kMaxTokens) return fail(MOE_EUNSUPPORTED, "B above 2^20 is not supported");
     if (misaligned(a.x, 16) || misaligned(a.y, 16)) return fail(MOE_EINVAL, "x and y must be 16-byte aligned");
@@ -317,7 +317,10 @@ int check_workspace(const void* ws, size_t have, size_t need) {
     return MOE_OK;
 }
 
-bool proj_sizes_ok(int B, int max_rank) { return B >= 1 && B <= moe::kMaxTokens && max_rank >= 0 && max_rank <= moe::kMaxLoraRank; }
+bool proj_sizes_ok(int B, int H, int O, int max_rank) {
+    return B >= 1 && B <= moe::kMaxTokens && H >= 1 && H <= 16384 && O >= 1 && O <= 16384 && max_rank >= 0 &&
+           max_rank <= moe::kMaxLoraRank;
+}
 
 }  // namespace
 
@@ -349,8 +352,8 @@ MOE_API int moe_lora_publish(moe_lora_handle* table, int i, const moe_lora_handl
 }
 
 MOE_API size_t moe_lora_workspace_bytes(int B, int H, int O, int max_rank, int x_dtype, int y_dtype) {
-    (void)H; (void)O; (void)x_dtype; (void)y_dtype;
-    return proj_sizes_ok(B, max_rank) ? moe::lora_workspace_bytes(B, padded_rank(max_rank)) : 0;
+    (void)y_dtype;
+    return proj_sizes_ok(B, H, O, max_rank) ? moe::lora_workspace_bytes(B, H, padded_rank(max_rank), x_dtype) : 0;
 }
 
 MOE_API int moe_lora_linear(const void* w, const moe_lora_handle* table, int n_adapters, int max_rank,
@@ -361,9 +364,9 @@ MOE_API int moe_lora_linear(const void* w, const moe_lora_handle* table, int n_a
     moe::ProjArgs a{};
     a.w[0] = w; a.table[0] = table; a.adapter = table ? adapter : nullptr;
     a.n_adapters = n_adapters; a.max_rank = table ? max_rank : 0;
-    a.x = x; a.x_dtype = x_dtype; a.B = B; a.H = H; a.O = O;
-    a.n_valid = n_valid; a.y = y; a.y_dtype = y_dtype; a.accumulate = accumulate != 0;
-    int st = check_proj(a, table != nullptr);
+    a.x = x; a.x_kind = x_dtype == MOE_DT_F32 ? moe::kActF32 : moe::kActBf16; a.B = B; a.H = H; a.O = O;
+    a.n_valid = n_valid; a.y = y; a.y_kind = y_dtype == MOE_DT_F32 ? moe::kActF32 : moe::kActBf16; a.accumulate = accumulate != 0;
+    int st = check_proj(a, x_dtype, y_dtype, table != nullptr);
     if (st) return st;
     if (H < 32 || H % 32) return fail(MOE_EINVAL, "H must be a positive multiple of 32");
     if (O < 16 || O % 16) return fail(MOE_EINVAL, "O must be a positive multiple of 16");
@@ -375,8 +378,9 @@ MOE_API int moe_lora_linear(const void* w, const moe_lora_handle* table, int n_a
 }
 
 MOE_API size_t moe_shared_ffn_workspace_bytes(int B, int H, int I, int max_rank, int x_dtype, int y_dtype) {
-    (void)H; (void)x_dtype;
-    return proj_sizes_ok(B, max_rank) && I >= 1 ? moe::shared_ffn_workspace_bytes(B, I, padded_rank(max_rank), y_dtype) : 0;
+    return proj_sizes_ok(B, H, I, max_rank)
+               ? moe::shared_ffn_workspace_bytes(B, H, I, padded_rank(max_rank), x_dtype, y_dtype)
+               : 0;
 }
 
 MOE_API int moe_shared_ffn(const moe_expert_handle* shared, const moe_lora_handle* t_gate,
@@ -395,9 +399,9 @@ MOE_API int moe_shared_ffn(const moe_expert_handle* shared, const moe_lora_handl
     a.table[0] = t_gate; a.table[1] = t_up;
     a.adapter = any ? adapter : nullptr;
     a.n_adapters = n_adapters; a.max_rank = any ? max_rank : 0;
-    a.x = x; a.x_dtype = x_dtype; a.B = B; a.H = H; a.O = I;
-    a.n_valid = n_valid; a.y = y; a.y_dtype = y_dtype; a.accumulate = accumulate != 0;
-    int st = check_proj(a, any);
+    a.x = x; a.x_kind = x_dtype == MOE_DT_F32 ? moe::kActF32 : moe::kActBf16; a.B = B; a.H = H; a.O = I;
+    a.n_valid = n_valid; a.y = y; a.y_kind = y_dtype == MOE_DT_F32 ? moe::kActF32 : moe::kActBf16; a.accumulate = accumulate != 0;
+    int st = check_proj(a, x_dtype, y_dtype, any);
     if (st) return st;
     if (H < 32 || H % 32 || I < 32 || I % 32) return fail(MOE_EINVAL, "H and I must be positive multiples of 32");
     if (H > 16384 || I > 16384) return fail(MOE_EUNSUPPORTED, "H and I above 16384 are not supported");

@@ -120,20 +120,25 @@ hipError_t launch_route_grouped(const GroupedArgs& a, hipStream_t s);
 // One projection with adapters (or the gate/up pair: two matrices, tables and
 // v).  H input columns, O output rows.
 constexpr int kMaxLoraRank = 256;
+// How activations lie in memory: bf16 rows, fp32 rows, or the three bf16
+// terms of fp32 values as three planes of bf16 rows.
+enum ActKind { kActBf16, kActF32, kActPlanes };
 struct ProjArgs {
     const void* w[2];
     const moe_lora_handle* table[2];   // null: no adapters on that matrix
     const int32_t* adapter;            // null: none
     int n_adapters, max_rank;
     const void* x;
-    int x_dtype, B, H, O;
+    int x_kind, B, H, O;
+    size_t x_plane;                    // bytes between planes
     const int32_t* n_valid;
     void* y;
-    int y_dtype, accumulate;
+    int y_kind, accumulate;
+    size_t y_plane;
     float* v[2];                       // [B, max_rank]: scale A x
 };
-size_t lora_workspace_bytes(int B, int max_rank);
-size_t shared_ffn_workspace_bytes(int B, int I, int max_rank, int y_dtype);
+size_t lora_workspace_bytes(int B, int H, int max_rank, int x_dtype);
+size_t shared_ffn_workspace_bytes(int B, int H, int I, int max_rank, int x_dtype, int y_dtype);
 hipError_t launch_lora_linear(ProjArgs a, void* ws, hipStream_t s);
 hipError_t launch_shared_ffn(ProjArgs gate_up, const void* w_down, const moe_lora_handle* t_down, void* ws,
                              hipStream_t s);

@@ -70,23 +70,25 @@ __device__ __forceinline__ void split(const float (&f)[2 * P], uint32_t (&t)[T][
 }
 
 // One activation fragment: lane (n = l % 16, q = l / 16) holds columns
-// c .. c + 7 of its token, as the bf16 terms that enter the product.
-template <typename XT>
+// c .. c + 7 of its token, as the bf16 terms that enter the product: bf16
+// rows (one term), fp32 rows (three, cut in registers) or three bf16 planes
+// that hold the cut terms already.
+template <int XK>
 struct Frag;
 template <>
-struct Frag<uint16_t> {
-    static constexpr int kTerms = 1;
+struct Frag<kActBf16> {
+    static constexpr int kTerms = 1, kTileBytes = 64, kLaneBytes = 16;
     u32x4 raw;
-    __device__ void load(const uint16_t* p) { raw = *reinterpret_cast<const u32x4*>(p); }
+    __device__ void load(const char* p, size_t) { raw = *reinterpret_cast<const u32x4*>(p); }
     __device__ void terms(u32x4 (&t)[1]) const { t[0] = raw; }
 };
 template <>
-struct Frag<float> {
-    static constexpr int kTerms = 3;
+struct Frag<kActF32> {
+    static constexpr int kTerms = 3, kTileBytes = 128, kLaneBytes = 32;
     f32x4 lo, hi;
-    __device__ void load(const float* p) {
+    __device__ void load(const char* p, size_t) {
         lo = *reinterpret_cast<const f32x4*>(p);
-        hi = *reinterpret_cast<const f32x4*>(p + 4);
+        hi = *reinterpret_cast<const f32x4*>(p + 16);
     }
     __device__ void terms(u32x4 (&t)[3]) const {
         const float f[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
@@ -96,6 +98,25 @@ struct Frag<float> {
         for (int i = 0; i < 3; ++i) t[i] = u32x4{s[i][0], s[i][1], s[i][2], s[i][3]};
     }
 };
+template <>
+struct Frag<kActPlanes> {
+    static constexpr int kTerms = 3, kTileBytes = 64, kLaneBytes = 16;
+    u32x4 raw[3];
+    __device__ void load(const char* p, size_t plane) {
+#pragma unroll
+        for (int i = 0; i < 3; ++i) raw[i] = *reinterpret_cast<const u32x4*>(p + i * plane);
+    }
+    __device__ void terms(u32x4 (&t)[3]) const {
+#pragma unroll
+        for (int i = 0; i < 3; ++i) t[i] = raw[i];
+    }
+};
+// Row i of x, the lane's part of it.
+template <int XK>
+__device__ __forceinline__ const char* x_row(const ProjArgs& a, int i, int q) {
+    return static_cast<const char*>(a.x) + static_cast<size_t>(i) * a.H * (Frag<XK>::kTileBytes / 32) +
+           q * Frag<XK>::kLaneBytes;
+}
 
 __device__ __forceinline__ int real_tokens(const ProjArgs& a) {
     return a.n_valid != nullptr ? min(max(*a.n_valid, 0), a.B) : a.B;
@@ -113,109 +134,225 @@ __device__ __forceinline__ int rank_blocks(const moe_lora_handle& h, int max_ran
 }
 
 // ---------------------------------------------------------------------------
-// shrink: v[i, r] = scale * sum_h A[r, h] x[i, h].  One workgroup per (token
-// of a tile of 16 that is the first with its adapter, rank block, table); its
-// four waves split H and add their sums in LDS in a fixed order.
+// shrink: v[i, r] = scale * sum_h A[r, h] x[i, h].  Tokens of one adapter are
+// scattered over the batch, so a workgroup gathers its own: it scans the ids
+// of a chunk of kChunk tokens, keeps those of its adapter whose place among
+// them falls into its part of 16 NT, and multiplies them with RBN rank blocks
+// of A; its W waves take the columns' tiles in turn and add their sums in LDS
+// in a fixed order.  A workgroup without tokens ends after the scan.
+// Workgroups are laid out over the table's entries, or over the chunk's
+// tokens (the first token of each adapter stands for it) where those are fewer.
 // ---------------------------------------------------------------------------
-constexpr int kShrinkWaves = 4;
+constexpr int kChunk = 2048;
 
-template <typename XT>
-__global__ __launch_bounds__(kShrinkWaves * kWave) void shrink_kernel(ProjArgs a) {
-    __shared__ f32x4 part[kShrinkWaves][kWave];
-    const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
+template <int XK, int NT, int RBN, int W>
+__global__ __launch_bounds__(W* kWave) void shrink_kernel(ProjArgs a, int parts, int by_token) {
+    __shared__ f32x4 part[W][RBN * NT][kWave];
+    __shared__ int tok_s[16 * NT];
+    __shared__ int wave_n[W];
+    const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
     const int n = lane & 15, q = lane >> 4;
-    const int i0 = (blockIdx.x >> 4) * 16, slot = blockIdx.x & 15;
     const int B_real = real_tokens(a);
-    const moe_lora_handle* table = a.table[blockIdx.z];
-    if (i0 + slot >= B_real || table == nullptr) return;
-    const int id = adapter_of(a, i0 + n, B_real);
-    const int ad = __builtin_amdgcn_readlane(id, slot);
-    if (ad < 0) return;
-    const uint64_t same = __ballot(id == ad) & 0xffffull;
-    if (__ffsll(static_cast<unsigned long long>(same)) - 1 != slot) return;
+    const int pieces = (a.max_rank / 16 + RBN - 1) / RBN;   // of rank blocks
+    const int t_id = blockIdx.z / pieces, rb0 = (blockIdx.z % pieces) * RBN;
+    const int part_id = blockIdx.y % parts, c0 = (blockIdx.y / parts) * kChunk;
+    const int c1 = min(c0 + kChunk, B_real);
+    const moe_lora_handle* table = a.table[t_id];
+    if (table == nullptr || c0 >= c1) return;
+    int ad = blockIdx.x;
+    if (by_token) {   // this token's adapter, if no earlier token of the chunk has it
+        if (c0 + static_cast<int>(blockIdx.x) >= c1) return;
+        ad = a.adapter[c0 + blockIdx.x];
+        if (ad < 0 || ad >= a.n_adapters) return;
+        int dup = 0;
+        for (int i = c0 + tid; i < c0 + static_cast<int>(blockIdx.x); i += W * kWave) dup |= a.adapter[i] == ad;
+        if (__syncthreads_or(dup)) return;
+    }
     const moe_lora_handle h = table[ad];
-    const int rb = blockIdx.y;
-    if (rb >= rank_blocks(h, a.max_rank)) return;
+    const int nb = rank_blocks(h, a.max_rank);
+    if (rb0 >= nb) return;
+
+    // the chunk's tokens of this adapter, in order: places part_id 16 NT ..
+    if (tid < 16 * NT) tok_s[tid] = -1;
+    int base = -part_id * 16 * NT;   // place of the next match, relative to this part
+    for (int i0 = c0; i0 < c1; i0 += W * kWave) {
+        const int i = i0 + tid;
+        const bool m = i < c1 && a.adapter[i] == ad;
+        const uint64_t b = __ballot(m);
+        if (lane == 0) wave_n[wave] = __popcll(b);
+        __syncthreads();
+        int at = base + __popcll(b & ((1ull << lane) - 1ull));
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+            at += w < wave ? wave_n[w] : 0;
+            base += wave_n[w];
+        }
+        if (m && at >= 0 && at < 16 * NT) tok_s[at] = i;
+        __syncthreads();
+        if (base >= 16 * NT) break;
+    }
+    const int have = min(base, 16 * NT);
+    if (have <= 0) return;
 
     const int S = a.H / 32;
-    const char* A = static_cast<const char*>(h.a) + (static_cast<size_t>(rb) * S) * 1024 + lane * 16;
-    const XT* x = static_cast<const XT*>(a.x) + static_cast<size_t>(min(i0 + n, B_real - 1)) * a.H + 8 * q;
-    f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll 4
-    for (int s = wave; s < S; s += kShrinkWaves) {
-        const u32x4 w = *reinterpret_cast<const u32x4*>(A + static_cast<size_t>(s) * 1024);
-        Frag<XT> f;
-        f.load(x + s * 32);
-        u32x4 t[Frag<XT>::kTerms];
-        f.terms(t);
+    const char* A[RBN];
 #pragma unroll
-        for (int k = Frag<XT>::kTerms - 1; k >= 0; --k) acc = mma32(w, t[k], acc);
-    }
-    part[wave][lane] = acc;
-    __syncthreads();
-    if (wave != 0 || id != ad) return;
-    f32x4 v = part[0][lane];
+    for (int r = 0; r < RBN; ++r)
+        A[r] = static_cast<const char*>(h.a) + static_cast<size_t>(min(rb0 + r, nb - 1)) * S * 1024 + lane * 16;
+    const char* xp[NT];
 #pragma unroll
-    for (int w = 1; w < kShrinkWaves; ++w) v += part[w][lane];
-    float* out = a.v[blockIdx.z] + static_cast<size_t>(i0 + n) * a.max_rank + 16 * rb + 4 * q;
-    *reinterpret_cast<f32x4*>(out) = v * h.scale;
-}
-
-// Adds the adapters' part to the accumulator of row block ob and the 16
-// tokens whose adapters are `id` (lane 16 q + n: token n); v_row is the lane's
-// token's row of v.
-template <int VT>
-__device__ __forceinline__ f32x4 expand(const ProjArgs& a, int m, int ob, int id, const float* v_row, f32x4 acc) {
-    const int lane = threadIdx.x & (kWave - 1), q = lane >> 4;
-    const moe_lora_handle* table = a.table[m];
-    if (table == nullptr) return acc;
-    uint32_t rem = static_cast<uint32_t>(__ballot(id >= 0)) & 0xffffu;
-    while (rem != 0u) {
-        const int ad = __builtin_amdgcn_readlane(id, __ffs(rem) - 1);
-        const bool mine = id == ad;
-        rem &= ~static_cast<uint32_t>(__ballot(mine));
-        const moe_lora_handle h = table[ad];
-        const int nb = rank_blocks(h, a.max_rank);
-        const char* b = static_cast<const char*>(h.b) + (static_cast<size_t>(ob) * nb) * 512 + lane * 8;
-        for (int r = 0; r < nb; ++r) {
-            const u32x2 bw = *reinterpret_cast<const u32x2*>(b + r * 512);
-            float f[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-            if (mine) {
-                const f32x4 v = *reinterpret_cast<const f32x4*>(v_row + 16 * r + 4 * q);
-                f[0] = v.x; f[1] = v.y; f[2] = v.z; f[3] = v.w;
-            }
-            uint32_t t[VT][2];
-            split<VT, 2>(f, t);
+    for (int t = 0; t < NT; ++t) xp[t] = x_row<XK>(a, tok_s[min(16 * t + n, have - 1)], q);
+    f32x4 acc[RBN][NT];
 #pragma unroll
-            for (int k = VT - 1; k >= 0; --k) acc = mma16(bw, u32x2{t[k][0], t[k][1]}, acc);
+    for (int r = 0; r < RBN; ++r)
+#pragma unroll
+        for (int t = 0; t < NT; ++t) acc[r][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    constexpr int kU = (RBN + NT) * (Frag<XK>::kTerms > 1 ? 2 : 1) > 4 ? 2 : 4;
+    const int nt = (have + 15) / 16;
+#pragma unroll kU
+    for (int s = wave; s < S; s += W) {
+        u32x4 w[RBN];
+#pragma unroll
+        for (int r = 0; r < RBN; ++r) w[r] = *reinterpret_cast<const u32x4*>(A[r] + static_cast<size_t>(s) * 1024);
+        Frag<XK> f[NT];
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+            if (t < nt) f[t].load(xp[t] + static_cast<size_t>(s) * Frag<XK>::kTileBytes, a.x_plane);
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            if (t >= nt) continue;
+            u32x4 x[Frag<XK>::kTerms];
+            f[t].terms(x);
+#pragma unroll
+            for (int k = Frag<XK>::kTerms - 1; k >= 0; --k)
+#pragma unroll
+                for (int r = 0; r < RBN; ++r) acc[r][t] = mma32(w[r], x[k], acc[r][t]);
         }
     }
-    return acc;
+#pragma unroll
+    for (int r = 0; r < RBN; ++r)
+#pragma unroll
+        for (int t = 0; t < NT; ++t) part[wave][r * NT + t][lane] = acc[r][t];
+    __syncthreads();
+    for (int p = wave; p < RBN * NT; p += W) {
+        const int r = p / NT, t = p % NT;
+        if (rb0 + r >= nb || 16 * t + n >= have) continue;
+        f32x4 v = part[0][p][lane];
+#pragma unroll
+        for (int w = 1; w < W; ++w) v += part[w][p][lane];
+        float* out = a.v[t_id] + static_cast<size_t>(tok_s[16 * t + n]) * a.max_rank + 16 * (rb0 + r) + 4 * q;
+        *reinterpret_cast<f32x4*>(out) = v * h.scale;
+    }
+}
+
+// Rank block r of the lane's token's v as bf16 terms (zero where !mine).
+template <int VT>
+__device__ __forceinline__ void v_terms(const float* v_row, int r, int q, bool mine, u32x2 (&out)[VT]) {
+    f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (mine) v = *reinterpret_cast<const f32x4*>(v_row + 16 * r + 4 * q);
+    const float f[4] = {v.x, v.y, v.z, v.w};
+    uint32_t t[VT][2];
+    split<VT, 2>(f, t);
+#pragma unroll
+    for (int k = 0; k < VT; ++k) out[k] = u32x2{t[k][0], t[k][1]};
+}
+
+// Adds B_a v to the accumulators of MB row blocks and NB tiles of 16 tokens
+// (i0 the first token), one adapter of those tokens after the other.  Of
+// adapter d's rank blocks r those with (d + r) mod step == first (step a power
+// of two): which wave adds a token's part does not depend on the other
+// tokens.  ob(j): row block of accumulator row j, mat(j): its matrix.
+template <int VT, int MB, int NB, typename Ob, typename Mat>
+__device__ __forceinline__ void expand(const ProjArgs& a, int i0, int B_real, int first, int step,
+                                       f32x4 (&acc)[MB][NB], Ob ob, Mat mat) {
+    static_assert(NB <= 4, "a token per lane");
+    if (a.adapter == nullptr) return;
+    const int lane = threadIdx.x & (kWave - 1), n = lane & 15, q = lane >> 4;
+    const int id = lane < 16 * NB ? adapter_of(a, i0 + lane, B_real) : -1;   // lane = token
+    uint64_t rem = __ballot(id >= 0);
+    while (rem != 0ull) {
+        const int ad = __builtin_amdgcn_readlane(id, __ffsll(static_cast<unsigned long long>(rem)) - 1);
+        const uint64_t who = __ballot(id == ad);
+        rem &= ~who;
+        constexpr bool kTwo = MB > 1;
+        moe_lora_handle h[2];
+        int nb[2] = {0, 0};
+#pragma unroll
+        for (int m = 0; m < (kTwo ? 2 : 1); ++m)
+            if (a.table[m] != nullptr) {
+                h[m] = a.table[m][ad];
+                nb[m] = rank_blocks(h[m], a.max_rank);
+            }
+        const int most = max(nb[0], nb[1]);
+        for (int r = (first - ad) & (step - 1); r < most; r += step) {
+            u32x2 b[MB];
+#pragma unroll
+            for (int j = 0; j < MB; ++j) {
+                const int m = mat(j);
+                b[j] = u32x2{0u, 0u};
+                if (r < nb[m])
+                    b[j] = *reinterpret_cast<const u32x2*>(static_cast<const char*>(h[m].b) +
+                                                           (static_cast<size_t>(ob(j)) * nb[m] + r) * 512 + lane * 8);
+            }
+#pragma unroll
+            for (int t = 0; t < NB; ++t) {
+                if (((who >> (16 * t)) & 0xffffull) == 0ull) continue;
+                const bool mine = (who >> (16 * t + n)) & 1ull;
+                const size_t row = static_cast<size_t>(min(i0 + 16 * t + n, B_real - 1)) * a.max_rank;
+#pragma unroll
+                for (int m = 0; m < (kTwo ? 2 : 1); ++m) {
+                    if (r >= nb[m]) continue;
+                    u32x2 v[VT];
+                    v_terms<VT>(a.v[m] + row, r, q, mine, v);
+#pragma unroll
+                    for (int j = 0; j < MB; ++j) {
+                        if (mat(j) != m) continue;
+#pragma unroll
+                        for (int k = VT - 1; k >= 0; --k) acc[j][t] = mma16(b[j], v[k], acc[j][t]);
+                    }
+                }
+            }
+        }
+    }
 }
 
 __device__ __forceinline__ float silu(float z) { return z / (1.0f + __expf(-z)); }
 
-// Four consecutive outputs of one token.
-__device__ __forceinline__ void store4(float* p, f32x4 v, int accumulate) {
-    if (accumulate) v += *reinterpret_cast<const f32x4*>(p);
-    *reinterpret_cast<f32x4*>(p) = v;
-}
-__device__ __forceinline__ void store4(uint16_t* p, f32x4 v, int) {
+// Four consecutive outputs (columns c .. c + 3) of token i.
+template <int YK>
+__device__ __forceinline__ void store4(const ProjArgs& a, int i, int c, f32x4 v) {
     typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
-    *reinterpret_cast<u32x2*>(p) = __builtin_bit_cast(u32x2, __builtin_convertvector(v, bf16x4));
+    const size_t at = static_cast<size_t>(i) * a.O + c;
+    if constexpr (YK == kActF32) {
+        float* p = static_cast<float*>(a.y) + at;
+        if (a.accumulate) v += *reinterpret_cast<const f32x4*>(p);
+        *reinterpret_cast<f32x4*>(p) = v;
+    } else if constexpr (YK == kActBf16) {
+        *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(a.y) + at) =
+            __builtin_bit_cast(u32x2, __builtin_convertvector(v, bf16x4));
+    } else {
+        const float f[4] = {v.x, v.y, v.z, v.w};
+        uint32_t t[3][2];
+        split<3, 2>(f, t);
+#pragma unroll
+        for (int k = 0; k < 3; ++k)
+            *reinterpret_cast<u32x2*>(static_cast<char*>(a.y) + k * a.y_plane + at * 2) = u32x2{t[k][0], t[k][1]};
+    }
 }
+template <int YK>
+constexpr int v_terms_for() { return YK == kActBf16 ? 2 : 3; }
 
 // ---------------------------------------------------------------------------
-// Streaming projection: a workgroup owns RB row blocks of 16 outputs (of NM
-// matrices: 2 = gate and up, whose result is silu(g) u) and NT tiles of 16
-// tokens; its W waves take the columns' tiles in turn and add their sums in
-// LDS in a fixed order.
+// Streaming projection, for few tokens: a workgroup owns RB row blocks of 16
+// outputs (of NM matrices: 2 = gate and up, whose result is silu(g) u) and NT
+// tiles of 16 tokens.  Its W waves take the columns' tiles in turn, and the
+// adapters of the tokens in turn, and add their sums in LDS in a fixed order.
 // ---------------------------------------------------------------------------
-template <typename XT, typename YT, int NM, int NT, int RB, int W>
+template <int XK, int YK, int NM, int NT, int RB, int W, int U>
 __global__ __launch_bounds__(W* kWave) void proj_stream_kernel(ProjArgs a) {
-    constexpr int VT = sizeof(YT) == 4 ? 3 : 2;
-    constexpr int TT = Frag<XT>::kTerms;
-    __shared__ f32x4 part[W][NM * RB * NT][kWave];
+    constexpr int TT = Frag<XK>::kTerms;
+    constexpr int MB = NM * RB;
+    __shared__ f32x4 part[W][MB * NT][kWave];
     const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
     const int n = lane & 15, q = lane >> 4;
     const int B_real = real_tokens(a);
@@ -224,35 +361,28 @@ __global__ __launch_bounds__(W* kWave) void proj_stream_kernel(ProjArgs a) {
     const int ob0 = blockIdx.x * RB, blocks = a.O / 16;
     const int S = a.H / 32;
 
-    const char* wp[NM][RB];
+    const char* wp[MB];
 #pragma unroll
-    for (int m = 0; m < NM; ++m)
+    for (int j = 0; j < MB; ++j)
+        wp[j] = static_cast<const char*>(a.w[j / RB]) +
+                static_cast<size_t>(min(ob0 + j % RB, blocks - 1)) * S * 1024 + lane * 16;
+    const char* xp[NT];
 #pragma unroll
-        for (int r = 0; r < RB; ++r)
-            wp[m][r] = static_cast<const char*>(a.w[m]) + (static_cast<size_t>(min(ob0 + r, blocks - 1)) * S) * 1024 +
-                       lane * 16;
-    const XT* xp[NT];
-#pragma unroll
-    for (int t = 0; t < NT; ++t)
-        xp[t] = static_cast<const XT*>(a.x) + static_cast<size_t>(min(i0 + 16 * t + n, B_real - 1)) * a.H + 8 * q;
+    for (int t = 0; t < NT; ++t) xp[t] = x_row<XK>(a, min(i0 + 16 * t + n, B_real - 1), q);
 
-    f32x4 acc[NM][RB][NT];
+    f32x4 acc[MB][NT];
 #pragma unroll
-    for (int m = 0; m < NM; ++m)
+    for (int j = 0; j < MB; ++j)
 #pragma unroll
-        for (int r = 0; r < RB; ++r)
-#pragma unroll
-            for (int t = 0; t < NT; ++t) acc[m][r][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll 2
+        for (int t = 0; t < NT; ++t) acc[j][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll U
     for (int s = wave; s < S; s += W) {
-        u32x4 w[NM][RB];
-        Frag<XT> f[NT];
+        u32x4 w[MB];
+        Frag<XK> f[NT];
 #pragma unroll
-        for (int m = 0; m < NM; ++m)
+        for (int j = 0; j < MB; ++j) w[j] = *reinterpret_cast<const u32x4*>(wp[j] + static_cast<size_t>(s) * 1024);
 #pragma unroll
-            for (int r = 0; r < RB; ++r) w[m][r] = *reinterpret_cast<const u32x4*>(wp[m][r] + static_cast<size_t>(s) * 1024);
-#pragma unroll
-        for (int t = 0; t < NT; ++t) f[t].load(xp[t] + s * 32);
+        for (int t = 0; t < NT; ++t) f[t].load(xp[t] + static_cast<size_t>(s) * Frag<XK>::kTileBytes, a.x_plane);
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
             u32x4 x[TT];
@@ -260,72 +390,227 @@ __global__ __launch_bounds__(W* kWave) void proj_stream_kernel(ProjArgs a) {
 #pragma unroll
             for (int k = TT - 1; k >= 0; --k)
 #pragma unroll
-                for (int m = 0; m < NM; ++m)
-#pragma unroll
-                    for (int r = 0; r < RB; ++r) acc[m][r][t] = mma32(w[m][r], x[k], acc[m][r][t]);
+                for (int j = 0; j < MB; ++j) acc[j][t] = mma32(w[j], x[k], acc[j][t]);
         }
     }
+    expand<v_terms_for<YK>()>(a, i0, B_real, wave, W, acc, [&](int j) { return min(ob0 + j % RB, blocks - 1); },
+                              [&](int j) { return j / RB; });
 #pragma unroll
-    for (int m = 0; m < NM; ++m)
+    for (int j = 0; j < MB; ++j)
 #pragma unroll
-        for (int r = 0; r < RB; ++r)
-#pragma unroll
-            for (int t = 0; t < NT; ++t) part[wave][(m * RB + r) * NT + t][lane] = acc[m][r][t];
+        for (int t = 0; t < NT; ++t) part[wave][j * NT + t][lane] = acc[j][t];
     __syncthreads();
     for (int p = wave; p < RB * NT; p += W) {
         const int r = p / NT, t = p % NT;
         const int ob = ob0 + r, i = i0 + 16 * t + n;
-        if (ob >= blocks || i0 + 16 * t >= B_real) continue;
-        const int id = adapter_of(a, i, B_real);
+        if (ob >= blocks || i >= B_real) continue;
         f32x4 sum[NM];
 #pragma unroll
         for (int m = 0; m < NM; ++m) {
             sum[m] = part[0][m * RB * NT + p][lane];
 #pragma unroll
             for (int w = 1; w < W; ++w) sum[m] += part[w][m * RB * NT + p][lane];
-            sum[m] = expand<VT>(a, m, ob, id, a.v[m] + static_cast<size_t>(min(i, B_real - 1)) * a.max_rank, sum[m]);
         }
         if constexpr (NM == 2) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) sum[0][j] = silu(sum[0][j]) * sum[1][j];
         }
-        if (i < B_real) store4(static_cast<YT*>(a.y) + static_cast<size_t>(i) * a.O + 16 * ob + 4 * q, sum[0], a.accumulate);
+        store4<YK>(a, i, 16 * ob + 4 * q, sum[0]);
     }
 }
 
-template <typename XT, typename YT, int NM>
-void launch_proj(const ProjArgs& a, hipStream_t s) {
-    const int blocks = a.O / 16;
-    if (a.B <= 16) {
-        proj_stream_kernel<XT, YT, NM, 1, 1, 8><<<dim3(blocks, 1), 8 * kWave, 0, s>>>(a);
-    } else {
-        proj_stream_kernel<XT, YT, NM, 2, 2, 4>
-            <<<dim3((blocks + 1) / 2, (a.B + 31) / 32), 4 * kWave, 0, s>>>(a);
+// ---------------------------------------------------------------------------
+// Tiled projection, for many tokens: a workgroup of WR x WC waves owns
+// 16 WR MB rows of W (for NM = 2 half of them gate rows and half the up rows of
+// the same outputs) and 16 WC NB tokens; a wave owns MB x NB blocks of 16 x 16
+// in accumulators.  Two column tiles at a time are copied to LDS in operand
+// order (a packed weight tile as it lies; of x the lane's 16 bytes of its
+// token's row), straight from memory (global_load_lds), into the half of a
+// double buffer that the products are not reading.
+// ---------------------------------------------------------------------------
+typedef __attribute__((address_space(1))) const void* gptr;
+typedef __attribute__((address_space(3))) void* lptr;
+
+template <int XK, int YK, int NM, int WR, int WC, int MB, int NB>
+__global__ __launch_bounds__(WR* WC* kWave) void proj_tile_kernel(ProjArgs a, int row_tiles, int tok_tiles) {
+    constexpr int NW = WR * WC;
+    constexpr int RT = WR * MB, CT = WC * NB;      // 1 KB tiles per 32 columns
+    constexpr int kStep = RT + CT;
+    constexpr int kStage = 2 * kStep * 1024;
+    constexpr int kPer = 2 * kStep / NW;           // tiles a wave copies per stage
+    static_assert(2 * kStep % NW == 0 && MB % NM == 0, "tile split");
+    constexpr int P = XK == kActPlanes ? 3 : 1;
+    __shared__ __align__(1024) char lds[2 * kStage];
+    const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
+    const int n = lane & 15, q = lane >> 4;
+    const int wr = wave / WC, wc = wave % WC;
+    const int B_real = real_tokens(a);
+    const int tile_r = blockIdx.x % row_tiles, tile_c = blockIdx.x / row_tiles;
+    const int i0 = tile_c * 16 * CT;
+    if (i0 >= B_real) return;
+    const int blocks = a.O / 16, S = a.H / 32, steps = P * S;
+    const int ob0 = tile_r * (RT / NM);
+    // output row block and matrix of row tile j of the workgroup
+    constexpr int kHalf = MB / NM;
+    auto mat_of = [](int j) { return NM == 1 ? 0 : (j % MB) / kHalf; };
+    auto ob_of = [&](int j) { return min(ob0 + (NM == 1 ? j : (j / MB) * kHalf + j % kHalf), blocks - 1); };
+
+    const char* src[kPer];
+#pragma unroll
+    for (int u = 0; u < kPer; ++u) {
+        const int slot = wave * kPer + u, j = slot >> 1;
+        if (j < RT)
+            src[u] = static_cast<const char*>(mat_of(j) ? a.w[1] : a.w[0]) + static_cast<size_t>(ob_of(j)) * S * 1024 +
+                     lane * 16;
+        else
+            src[u] = x_row<kActBf16>(a, min(i0 + 16 * (j - RT) + n, B_real - 1), q);
+    }
+    auto copy = [&](int it, int buf) {
+#pragma unroll
+        for (int u = 0; u < kPer; ++u) {
+            const int slot = wave * kPer + u, j = slot >> 1;
+            const int kk = min(2 * it + (slot & 1), steps - 1);
+            const int plane = P == 1 ? 0 : P - 1 - kk / S;   // the smallest term first
+            const int s = P == 1 ? kk : kk % S;
+            const char* g = src[u] + (j < RT ? static_cast<size_t>(s) * 1024
+                                             : static_cast<size_t>(s) * 64 + static_cast<size_t>(plane) * a.x_plane);
+            __builtin_amdgcn_global_load_lds((gptr)g, (lptr)(lds + buf * kStage + ((slot & 1) * kStep + j) * 1024), 16,
+                                             0, 0);
+        }
+    };
+
+    f32x4 acc[MB][NB];
+#pragma unroll
+    for (int j = 0; j < MB; ++j)
+#pragma unroll
+        for (int t = 0; t < NB; ++t) acc[j][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    copy(0, 0);
+    __syncthreads();
+    auto multiply = [&](int buf, int ks) {
+        const char* base = lds + buf * kStage + ks * kStep * 1024 + lane * 16;
+        u32x4 w[MB], x[NB];
+#pragma unroll
+        for (int t = 0; t < NB; ++t) x[t] = *reinterpret_cast<const u32x4*>(base + (RT + wc * NB + t) * 1024);
+#pragma unroll
+        for (int j = 0; j < MB; ++j) w[j] = *reinterpret_cast<const u32x4*>(base + (wr * MB + j) * 1024);
+#pragma unroll
+        for (int j = 0; j < MB; ++j)
+#pragma unroll
+            for (int t = 0; t < NB; ++t) acc[j][t] = mma32(w[j], x[t], acc[j][t]);
+    };
+    const int its = (steps + 1) / 2;
+    for (int it = 0; it + 1 < its; ++it) {
+        copy(it + 1, (it & 1) ^ 1);
+        multiply(it & 1, 0);
+        multiply(it & 1, 1);
+        __syncthreads();
+    }
+    multiply((its - 1) & 1, 0);
+    if ((steps & 1) == 0) multiply((its - 1) & 1, 1);
+    expand<v_terms_for<YK>()>(a, i0 + 16 * NB * wc, B_real, 0, 1, acc,
+                              [&](int j) { return ob_of(wr * MB + j); }, [&](int j) { return mat_of(j); });
+#pragma unroll
+    for (int j = 0; j < kHalf; ++j) {
+        const int ob = ob0 + wr * kHalf + j;
+        if (ob >= blocks) continue;
+#pragma unroll
+        for (int t = 0; t < NB; ++t) {
+            const int i = i0 + 16 * (NB * wc + t) + n;
+            f32x4 r = acc[j][t];
+            if constexpr (NM == 2) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) r[e] = silu(r[e]) * acc[j + kHalf][t][e];
+            }
+            if (i < B_real) store4<YK>(a, i, 16 * ob + 4 * q, r);
+        }
     }
 }
 
-template <typename XT>
+// fp32 rows cut into their three bf16 terms, as planes.
+__global__ __launch_bounds__(256) void planes_kernel(const f32x4* __restrict__ x, long chunks, u32x2* __restrict__ out,
+                                                     size_t plane) {
+    for (long c = static_cast<long>(blockIdx.x) * blockDim.x + threadIdx.x; c < chunks;
+         c += static_cast<long>(gridDim.x) * blockDim.x) {
+        const f32x4 v = x[c];
+        const float f[4] = {v.x, v.y, v.z, v.w};
+        uint32_t t[3][2];
+        split<3, 2>(f, t);
+#pragma unroll
+        for (int k = 0; k < 3; ++k) out[k * plane / 8 + c] = u32x2{t[k][0], t[k][1]};
+    }
+}
+
+constexpr int kStreamTokens = 128;   // up to this many: the streaming kernel
+constexpr int kRowTokens = 16;       // up to this many: fp32 rows are cut in registers
+
+template <int XK, int YK, int NM, int NT, int W, int U>
+void launch_stream(const ProjArgs& a, hipStream_t s) {
+    proj_stream_kernel<XK, YK, NM, NT, 1, W, U>
+        <<<dim3(a.O / 16, (a.B + 16 * NT - 1) / (16 * NT)), W * kWave, 0, s>>>(a);
+}
+template <int XK, int YK, int NM, int WR, int WC, int MB, int NB>
+hipError_t launch_tile(const ProjArgs& a, hipStream_t s) {
+    constexpr int kRows = 16 * WR * MB / NM, kTok = 16 * WC * NB;
+    const int rt = (a.O + kRows - 1) / kRows, ct = (a.B + kTok - 1) / kTok;
+    proj_tile_kernel<XK, YK, NM, WR, WC, MB, NB><<<static_cast<unsigned>(rt) * ct, WR * WC * kWave, 0, s>>>(a, rt, ct);
+    return hipGetLastError();
+}
+
+template <int XK, int YK, int NM>
+hipError_t launch_proj(const ProjArgs& a, hipStream_t s) {
+    if (a.B <= 16) launch_stream<XK, YK, NM, 1, 8, 4>(a, s);
+    else if constexpr (XK != kActF32) {
+        if (a.B <= 32) launch_stream<XK, YK, NM, 2, 8, 4>(a, s);
+        else if (a.B <= kStreamTokens) launch_stream<XK, YK, NM, 4, 8 / NM, 2>(a, s);
+        else {
+            const long big = (static_cast<long>(a.O) * NM + 255) / 256 * ((a.B + 255) / 256);
+            return big >= 128 ? launch_tile<XK, YK, NM, 2, 4, 8, 4>(a, s) : launch_tile<XK, YK, NM, 2, 2, 4, 4>(a, s);
+        }
+    }
+    return hipGetLastError();
+}
+
+template <int XK, int NT, int RBN, int W>
+void launch_shrink_as(const ProjArgs& a, int tables, hipStream_t s) {
+    const int chunk = std::min(a.B, kChunk), chunks = (a.B + kChunk - 1) / kChunk;
+    const int parts = (chunk + 16 * NT - 1) / (16 * NT);
+    const int by_token = a.n_adapters > chunk;
+    const int pieces = (a.max_rank / 16 + RBN - 1) / RBN;
+    shrink_kernel<XK, NT, RBN, W><<<dim3(by_token ? chunk : a.n_adapters, parts * chunks, pieces * tables), W * kWave, 0,
+                                    s>>>(a, parts, by_token);
+}
+template <int XK>
 void launch_shrink(const ProjArgs& a, int tables, hipStream_t s) {
-    shrink_kernel<XT><<<dim3((a.B + 15) / 16 * 16, a.max_rank / 16, tables), kShrinkWaves * kWave, 0, s>>>(a);
+    if (a.B <= 128) launch_shrink_as<XK, 1, 1, 8>(a, tables, s);
+    else launch_shrink_as<XK, 4, 2, 8>(a, tables, s);
 }
 
 // One projection (NM = 1) or the gate/up pair (NM = 2): shrink, then the product.
 template <int NM>
 hipError_t run_proj(const ProjArgs& a, hipStream_t s) {
-    if (a.adapter != nullptr && a.max_rank > 0 && (a.table[0] != nullptr || (NM == 2 && a.table[1] != nullptr))) {
-        if (a.x_dtype == MOE_DT_BF16) launch_shrink<uint16_t>(a, NM, s);
-        else launch_shrink<float>(a, NM, s);
+    if (a.adapter != nullptr && (a.table[0] != nullptr || (NM == 2 && a.table[1] != nullptr))) {
+        if (a.x_kind == kActBf16) launch_shrink<kActBf16>(a, NM, s);
+        else if (a.x_kind == kActPlanes) launch_shrink<kActPlanes>(a, NM, s);
+        else launch_shrink<kActF32>(a, NM, s);
         hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
-    if (a.x_dtype == MOE_DT_BF16) {
-        if (a.y_dtype == MOE_DT_BF16) launch_proj<uint16_t, uint16_t, NM>(a, s);
-        else launch_proj<uint16_t, float, NM>(a, s);
+#define MOE_PROJ(X_, Y_) \
+    if (a.x_kind == X_ && a.y_kind == Y_) return launch_proj<X_, Y_, NM>(a, s)
+    MOE_PROJ(kActBf16, kActBf16);
+    MOE_PROJ(kActF32, kActBf16);
+    MOE_PROJ(kActPlanes, kActBf16);
+    if constexpr (NM == 1) {
+        MOE_PROJ(kActBf16, kActF32);
+        MOE_PROJ(kActF32, kActF32);
+        MOE_PROJ(kActPlanes, kActF32);
     } else {
-        if (a.y_dtype == MOE_DT_BF16) launch_proj<float, uint16_t, NM>(a, s);
-        else launch_proj<float, float, NM>(a, s);
+        MOE_PROJ(kActBf16, kActPlanes);
+        MOE_PROJ(kActF32, kActPlanes);
+        MOE_PROJ(kActPlanes, kActPlanes);
     }
-    return hipGetLastError();
+#undef MOE_PROJ
+    return hipErrorInvalidValue;
 }
 
 // ---------------------------------------------------------------------------
@@ -364,40 +649,66 @@ __global__ void lora_publish_kernel(moe_lora_handle* table, int i, moe_lora_hand
 }
 
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
+size_t v_bytes(int B, int max_rank) { return up256(static_cast<size_t>(B) * max_rank * 4); }
+size_t x_planes_bytes(int B, int H, int x_dtype) {   // fp32 x of more than kRowTokens tokens
+    return x_dtype == MOE_DT_F32 && B > kRowTokens ? 3 * up256(static_cast<size_t>(B) * H * 2) : 0;
+}
+
+// Cut an fp32 x into planes at `ws` where the call's kernels read planes.
+hipError_t cut_x(ProjArgs& a, void* ws, hipStream_t s) {
+    if (a.x_kind != kActF32 || a.B <= kRowTokens) return hipSuccess;
+    const size_t plane = up256(static_cast<size_t>(a.B) * a.H * 2);
+    const long chunks = static_cast<long>(a.B) * a.H / 4;
+    planes_kernel<<<static_cast<unsigned>(std::min<long>((chunks + 255) / 256, 4096)), 256, 0, s>>>(
+        static_cast<const f32x4*>(a.x), chunks, static_cast<u32x2*>(ws), plane);
+    a.x = ws;
+    a.x_kind = kActPlanes;
+    a.x_plane = plane;
+    return hipGetLastError();
+}
 
 }  // namespace
 
-size_t lora_workspace_bytes(int B, int max_rank) {
-    return up256(static_cast<size_t>(B) * max_rank * 4);
+size_t lora_workspace_bytes(int B, int H, int max_rank, int x_dtype) {
+    return v_bytes(B, max_rank) + x_planes_bytes(B, H, x_dtype);
 }
 
-size_t shared_ffn_workspace_bytes(int B, int I, int max_rank, int y_dtype) {
-    return 3 * up256(static_cast<size_t>(B) * max_rank * 4) +
-           up256(static_cast<size_t>(B) * I * (y_dtype == MOE_DT_F32 ? 4 : 2));
+// v of gate, up and down, the planes of x, h (bf16, or three planes for an fp32 y).
+size_t shared_ffn_workspace_bytes(int B, int H, int I, int max_rank, int x_dtype, int y_dtype) {
+    return 3 * v_bytes(B, max_rank) + x_planes_bytes(B, H, x_dtype) +
+           (y_dtype == MOE_DT_F32 ? 3 : 1) * up256(static_cast<size_t>(B) * I * 2);
 }
 
 hipError_t launch_lora_linear(ProjArgs a, void* ws, hipStream_t s) {
     a.v[0] = static_cast<float*>(ws);
-    return run_proj<1>(a, s);
+    hipError_t e = cut_x(a, static_cast<char*>(ws) + v_bytes(a.B, a.max_rank), s);
+    return e != hipSuccess ? e : run_proj<1>(a, s);
 }
 
 hipError_t launch_shared_ffn(ProjArgs a, const void* w_down, const moe_lora_handle* t_down, void* ws, hipStream_t s) {
     char* p = static_cast<char*>(ws);
-    const size_t v_bytes = up256(static_cast<size_t>(a.B) * a.max_rank * 4);
+    const size_t vb = v_bytes(a.B, a.max_rank);
+    const size_t h_plane = up256(static_cast<size_t>(a.B) * a.O * 2);
     ProjArgs d = a;
     a.v[0] = reinterpret_cast<float*>(p);
-    a.v[1] = reinterpret_cast<float*>(p + v_bytes);
-    d.v[0] = reinterpret_cast<float*>(p + 2 * v_bytes);
+    a.v[1] = reinterpret_cast<float*>(p + vb);
+    d.v[0] = reinterpret_cast<float*>(p + 2 * vb);
+    char* x_planes = p + 3 * vb;
+    char* h = x_planes + x_planes_bytes(a.B, a.H, a.x_kind == kActF32 ? MOE_DT_F32 : MOE_DT_BF16);
+    a.y = h;
+    a.y_kind = a.y_kind == kActF32 ? kActPlanes : kActBf16;
+    a.y_plane = h_plane;
+    a.accumulate = 0;
     d.w[0] = w_down;
     d.table[0] = t_down;
     d.table[1] = nullptr;
-    d.x = p + 3 * v_bytes;
-    d.x_dtype = a.y_dtype;   // h is kept in the output's type
+    d.x = h;
+    d.x_kind = a.y_kind;
+    d.x_plane = h_plane;
     d.H = a.O;
     d.O = a.H;
-    a.y = p + 3 * v_bytes;
-    a.accumulate = 0;
-    hipError_t e = run_proj<2>(a, s);
+    hipError_t e = cut_x(a, x_planes, s);
+    if (e == hipSuccess) e = run_proj<2>(a, s);
     return e != hipSuccess ? e : run_proj<1>(d, s);
 }
 
