@@ -353,7 +353,7 @@ MOE_API int moe_lora_publish(moe_lora_handle* table, int i, const moe_lora_handl
 
 MOE_API size_t moe_lora_workspace_bytes(int B, int H, int O, int max_rank, int x_dtype, int y_dtype) {
     (void)y_dtype;
-    return proj_sizes_ok(B, H, O, max_rank) ? moe::lora_workspace_bytes(B, H, padded_rank(max_rank), x_dtype) : 0;
+    return proj_sizes_ok(B, H, O, max_rank) ? moe::lora_workspace_bytes(B, H, O, padded_rank(max_rank), x_dtype) : 0;
 }
 
 MOE_API int moe_lora_linear(const void* w, const moe_lora_handle* table, int n_adapters, int max_rank,

@@ -137,7 +137,7 @@ struct ProjArgs {
     size_t y_plane;
     float* v[2];                       // [B, max_rank]: scale A x
 };
-size_t lora_workspace_bytes(int B, int H, int max_rank, int x_dtype);
+size_t lora_workspace_bytes(int B, int H, int O, int max_rank, int x_dtype);
 size_t shared_ffn_workspace_bytes(int B, int H, int I, int max_rank, int x_dtype, int y_dtype);
 hipError_t launch_lora_linear(ProjArgs a, void* ws, hipStream_t s);
 hipError_t launch_shared_ffn(ProjArgs gate_up, const void* w_down, const moe_lora_handle* t_down, void* ws,

@@ -136,113 +136,133 @@ __device__ __forceinline__ int rank_blocks(const moe_lora_handle& h, int max_ran
 // ---------------------------------------------------------------------------
 // shrink: v[i, r] = scale * sum_h A[r, h] x[i, h].  Tokens of one adapter are
 // scattered over the batch, so a workgroup gathers its own: it scans the ids
-// of a chunk of kChunk tokens, keeps those of its adapter whose place among
-// them falls into its part of 16 NT, and multiplies them with RBN rank blocks
-// of A; its W waves take the columns' tiles in turn and add their sums in LDS
-// in a fixed order.  A workgroup without tokens ends after the scan.
-// Workgroups are laid out over the table's entries, or over the chunk's
-// tokens (the first token of each adapter stands for it) where those are fewer.
+// of a chunk of tokens [c0, c1), keeps those of its adapter whose place among
+// them falls into a part of 16 NT, and multiplies them with RBN rank blocks
+// of A; its W waves take pairs of the columns' tiles in turn (a pair is one
+// 128-byte line of a bf16 row) and add their sums in LDS in a fixed order.
 // ---------------------------------------------------------------------------
-constexpr int kChunk = 2048;
+template <int NT, int RBN, int W>
+struct ShrinkLds {
+    f32x4 part[W][RBN * NT][kWave];
+    int tok[16 * NT];
+    int wave_n[W];
+};
 
+// Parts first_part, first_part + step, .. (step 0: that part alone) of adapter
+// ad's tokens, rank blocks rb0 .. of table t_id.
 template <int XK, int NT, int RBN, int W>
-__global__ __launch_bounds__(W* kWave) void shrink_kernel(ProjArgs a, int parts, int by_token) {
-    __shared__ f32x4 part[W][RBN * NT][kWave];
-    __shared__ int tok_s[16 * NT];
-    __shared__ int wave_n[W];
+__device__ __forceinline__ void shrink_block(const ProjArgs& a, ShrinkLds<NT, RBN, W>& l, int t_id, int ad, int rb0,
+                                             int c0, int c1, int first_part, int step) {
     const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
     const int n = lane & 15, q = lane >> 4;
-    const int B_real = real_tokens(a);
-    const int pieces = (a.max_rank / 16 + RBN - 1) / RBN;   // of rank blocks
-    const int t_id = blockIdx.z / pieces, rb0 = (blockIdx.z % pieces) * RBN;
-    const int part_id = blockIdx.y % parts, c0 = (blockIdx.y / parts) * kChunk;
-    const int c1 = min(c0 + kChunk, B_real);
-    const moe_lora_handle* table = a.table[t_id];
-    if (table == nullptr || c0 >= c1) return;
-    int ad = blockIdx.x;
-    if (by_token) {   // this token's adapter, if no earlier token of the chunk has it
-        if (c0 + static_cast<int>(blockIdx.x) >= c1) return;
-        ad = a.adapter[c0 + blockIdx.x];
-        if (ad < 0 || ad >= a.n_adapters) return;
-        int dup = 0;
-        for (int i = c0 + tid; i < c0 + static_cast<int>(blockIdx.x); i += W * kWave) dup |= a.adapter[i] == ad;
-        if (__syncthreads_or(dup)) return;
-    }
-    const moe_lora_handle h = table[ad];
+    const moe_lora_handle h = a.table[t_id][ad];
     const int nb = rank_blocks(h, a.max_rank);
     if (rb0 >= nb) return;
-
-    // the chunk's tokens of this adapter, in order: places part_id 16 NT ..
-    if (tid < 16 * NT) tok_s[tid] = -1;
-    int base = -part_id * 16 * NT;   // place of the next match, relative to this part
-    for (int i0 = c0; i0 < c1; i0 += W * kWave) {
-        const int i = i0 + tid;
-        const bool m = i < c1 && a.adapter[i] == ad;
-        const uint64_t b = __ballot(m);
-        if (lane == 0) wave_n[wave] = __popcll(b);
-        __syncthreads();
-        int at = base + __popcll(b & ((1ull << lane) - 1ull));
-#pragma unroll
-        for (int w = 0; w < W; ++w) {
-            at += w < wave ? wave_n[w] : 0;
-            base += wave_n[w];
-        }
-        if (m && at >= 0 && at < 16 * NT) tok_s[at] = i;
-        __syncthreads();
-        if (base >= 16 * NT) break;
-    }
-    const int have = min(base, 16 * NT);
-    if (have <= 0) return;
-
     const int S = a.H / 32;
     const char* A[RBN];
 #pragma unroll
     for (int r = 0; r < RBN; ++r)
         A[r] = static_cast<const char*>(h.a) + static_cast<size_t>(min(rb0 + r, nb - 1)) * S * 1024 + lane * 16;
-    const char* xp[NT];
+    for (int part_id = first_part;; part_id += step) {
+        // the chunk's tokens of this adapter, in order: places part_id 16 NT ..
+        int base = -part_id * 16 * NT;   // place of the next match, relative to this part
+        for (int i0 = c0; i0 < c1; i0 += W * kWave) {
+            const int i = i0 + tid;
+            const bool m = i < c1 && a.adapter[i] == ad;
+            const uint64_t b = __ballot(m);
+            if (lane == 0) l.wave_n[wave] = __popcll(b);
+            __syncthreads();
+            int at = base + __popcll(b & ((1ull << lane) - 1ull));
 #pragma unroll
-    for (int t = 0; t < NT; ++t) xp[t] = x_row<XK>(a, tok_s[min(16 * t + n, have - 1)], q);
-    f32x4 acc[RBN][NT];
-#pragma unroll
-    for (int r = 0; r < RBN; ++r)
-#pragma unroll
-        for (int t = 0; t < NT; ++t) acc[r][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    constexpr int kU = (RBN + NT) * (Frag<XK>::kTerms > 1 ? 2 : 1) > 4 ? 2 : 4;
-    const int nt = (have + 15) / 16;
-#pragma unroll kU
-    for (int s = wave; s < S; s += W) {
-        u32x4 w[RBN];
-#pragma unroll
-        for (int r = 0; r < RBN; ++r) w[r] = *reinterpret_cast<const u32x4*>(A[r] + static_cast<size_t>(s) * 1024);
-        Frag<XK> f[NT];
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-            if (t < nt) f[t].load(xp[t] + static_cast<size_t>(s) * Frag<XK>::kTileBytes, a.x_plane);
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            if (t >= nt) continue;
-            u32x4 x[Frag<XK>::kTerms];
-            f[t].terms(x);
-#pragma unroll
-            for (int k = Frag<XK>::kTerms - 1; k >= 0; --k)
-#pragma unroll
-                for (int r = 0; r < RBN; ++r) acc[r][t] = mma32(w[r], x[k], acc[r][t]);
+            for (int w = 0; w < W; ++w) {
+                at += w < wave ? l.wave_n[w] : 0;
+                base += l.wave_n[w];
+            }
+            if (m && at >= 0 && at < 16 * NT) l.tok[at] = i;
+            __syncthreads();
+            if (base > 16 * NT) break;
         }
+        const int have = min(base, 16 * NT);
+        if (have <= 0) return;
+
+        const char* xp[NT];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) xp[t] = x_row<XK>(a, l.tok[min(16 * t + n, have - 1)], q);
+        f32x4 acc[RBN][NT];
+#pragma unroll
+        for (int r = 0; r < RBN; ++r)
+#pragma unroll
+            for (int t = 0; t < NT; ++t) acc[r][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        auto tile = [&](int s) {
+            u32x4 w[RBN];
+#pragma unroll
+            for (int r = 0; r < RBN; ++r) w[r] = *reinterpret_cast<const u32x4*>(A[r] + static_cast<size_t>(s) * 1024);
+            Frag<XK> f[NT];
+#pragma unroll
+            for (int t = 0; t < NT; ++t) f[t].load(xp[t] + static_cast<size_t>(s) * Frag<XK>::kTileBytes, a.x_plane);
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                u32x4 x[Frag<XK>::kTerms];
+                f[t].terms(x);
+#pragma unroll
+                for (int k = Frag<XK>::kTerms - 1; k >= 0; --k)
+#pragma unroll
+                    for (int r = 0; r < RBN; ++r) acc[r][t] = mma32(w[r], x[k], acc[r][t]);
+            }
+        };
+        constexpr int kU = Frag<XK>::kTerms > 1 || RBN * NT > 4 ? 1 : 2;
+        const int pairs = S / 2;
+#pragma unroll kU
+        for (int s = wave; s < pairs; s += W) {
+            tile(2 * s);
+            tile(2 * s + 1);
+        }
+        if ((S & 1) && wave == W - 1) tile(S - 1);
+#pragma unroll
+        for (int r = 0; r < RBN; ++r)
+#pragma unroll
+            for (int t = 0; t < NT; ++t) l.part[wave][r * NT + t][lane] = acc[r][t];
+        __syncthreads();
+        for (int p = wave; p < RBN * NT; p += W) {
+            const int r = p / NT, t = p % NT;
+            if (rb0 + r >= nb || 16 * t + n >= have) continue;
+            f32x4 v = l.part[0][p][lane];
+#pragma unroll
+            for (int w = 1; w < W; ++w) v += l.part[w][p][lane];
+            float* out = a.v[t_id] + static_cast<size_t>(l.tok[16 * t + n]) * a.max_rank + 16 * (rb0 + r) + 4 * q;
+            *reinterpret_cast<f32x4*>(out) = v * h.scale;
+        }
+        if (step == 0 || base <= 16 * NT) return;
+        __syncthreads();
     }
-#pragma unroll
-    for (int r = 0; r < RBN; ++r)
-#pragma unroll
-        for (int t = 0; t < NT; ++t) part[wave][r * NT + t][lane] = acc[r][t];
-    __syncthreads();
-    for (int p = wave; p < RBN * NT; p += W) {
-        const int r = p / NT, t = p % NT;
-        if (rb0 + r >= nb || 16 * t + n >= have) continue;
-        f32x4 v = part[0][p][lane];
-#pragma unroll
-        for (int w = 1; w < W; ++w) v += part[w][p][lane];
-        float* out = a.v[t_id] + static_cast<size_t>(tok_s[16 * t + n]) * a.max_rank + 16 * (rb0 + r) + 4 * q;
-        *reinterpret_cast<f32x4*>(out) = v * h.scale;
-    }
+}
+
+// Workgroups of a chunk are laid out over the table's entries, or over the
+// chunk's tokens (the first token of each adapter stands for it) where those
+// are fewer.  The adapter of place `at`, -1: none here.  Uniform over the
+// workgroup; every thread calls it.
+__device__ __forceinline__ int shrink_adapter(const ProjArgs& a, int at, int by_token, int c0, int c1) {
+    if (!by_token) return at;
+    if (c0 + at >= c1) return -1;
+    const int ad = a.adapter[c0 + at];
+    if (ad < 0 || ad >= a.n_adapters) return -1;
+    int dup = 0;
+    for (int i = c0 + static_cast<int>(threadIdx.x); i < c0 + at; i += blockDim.x) dup |= a.adapter[i] == ad;
+    return __syncthreads_or(dup) ? -1 : ad;
+}
+
+constexpr int kChunk = 2048;
+
+// grid: (places, parts x chunks, pieces of rank blocks x tables)
+template <int XK, int NT, int RBN, int W>
+__global__ __launch_bounds__(W* kWave) void shrink_kernel(ProjArgs a, int parts, int by_token) {
+    __shared__ ShrinkLds<NT, RBN, W> l;
+    const int pieces = (a.max_rank / 16 + RBN - 1) / RBN;
+    const int t_id = blockIdx.z / pieces, rb0 = (blockIdx.z % pieces) * RBN;
+    const int c0 = (blockIdx.y / parts) * kChunk, c1 = min(c0 + kChunk, real_tokens(a));
+    if (a.table[t_id] == nullptr || c0 >= c1) return;
+    const int ad = shrink_adapter(a, blockIdx.x, by_token, c0, c1);
+    if (ad >= 0) shrink_block<XK, NT, RBN, W>(a, l, t_id, ad, rb0, c0, c1, blockIdx.y % parts, 0);
 }
 
 // Rank block r of the lane's token's v as bf16 terms (zero where !mine).
@@ -307,8 +327,10 @@ __device__ __forceinline__ void expand(const ProjArgs& a, int i0, int B_real, in
 #pragma unroll
                     for (int j = 0; j < MB; ++j) {
                         if (mat(j) != m) continue;
+                        f32x4 sum = acc[j][t];
 #pragma unroll
-                        for (int k = VT - 1; k >= 0; --k) acc[j][t] = mma16(b[j], v[k], acc[j][t]);
+                        for (int k = VT - 1; k >= 0; --k) sum = mma16(b[j], v[k], sum);
+                        acc[j][t] = mine ? sum : acc[j][t];   // (a non-finite B stays with its own tokens)
                     }
                 }
             }
@@ -343,23 +365,186 @@ template <int YK>
 constexpr int v_terms_for() { return YK == kActBf16 ? 2 : 3; }
 
 // ---------------------------------------------------------------------------
-// Streaming projection, for few tokens: a workgroup owns RB row blocks of 16
-// outputs (of NM matrices: 2 = gate and up, whose result is silu(g) u) and NT
-// tiles of 16 tokens.  Its W waves take the columns' tiles in turn, and the
-// adapters of the tokens in turn, and add their sums in LDS in a fixed order.
+// At most 16 tokens whose adapters hold at most kFusedBlocks rank blocks
+// together (bounded by the call's sizes): one launch.  A workgroup owns 16
+// outputs (of NM matrices: 2 = gate and up, whose result is silu(g) u).  Its W
+// waves take the columns' tiles in turn, of W and of every A in use (each
+// workgroup forms A x again: that costs reads from the caches, and saves a
+// launch that every output would wait for), and add their sums in LDS in a
+// fixed order; B (A x) follows there.
 // ---------------------------------------------------------------------------
-template <int XK, int YK, int NM, int NT, int RB, int W, int U>
-__global__ __launch_bounds__(W* kWave) void proj_stream_kernel(ProjArgs a) {
-    constexpr int TT = Frag<XK>::kTerms;
-    constexpr int MB = NM * RB;
-    __shared__ f32x4 part[W][MB * NT][kWave];
+constexpr int kFusedBlocks = 4;
+
+template <int XK, int YK, int NM, int W, int U>
+__global__ __launch_bounds__(W* kWave) void proj_fused_kernel(ProjArgs a) {
+    constexpr int TT = Frag<XK>::kTerms, VT = v_terms_for<YK>(), D = kFusedBlocks;
+    constexpr int kTiles = NM * (1 + D);   // of matrix m: its outputs, then D products A x
+    __shared__ f32x4 part[W][kTiles][kWave];
     const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
     const int n = lane & 15, q = lane >> 4;
     const int B_real = real_tokens(a);
-    const int i0 = blockIdx.y * 16 * NT;
+    if (B_real <= 0) return;
+    const int ob = blockIdx.x, S = a.H / 32;
+    const char* w[NM];
+#pragma unroll
+    for (int m = 0; m < NM; ++m)
+        w[m] = static_cast<const char*>(a.w[m]) + static_cast<size_t>(ob) * S * 1024 + lane * 16;
+    const char* x = x_row<XK>(a, min(n, B_real - 1), q);
+
+    // the rank blocks in use: A's tiles, B's half tile of these outputs, tokens, scale
+    const char* ap[NM][D];
+    const char* bp[NM][D];
+    uint32_t who[NM][D];
+    float scale[NM][D];
+    int used[NM];
+    const int id = adapter_of(a, n, B_real);
+#pragma unroll
+    for (int m = 0; m < NM; ++m) {
+        uint32_t rem = a.table[m] != nullptr ? static_cast<uint32_t>(__ballot(id >= 0)) & 0xffffu : 0u, mask = 0u;
+        int r = 0, nb = 0;
+        moe_lora_handle h;
+        used[m] = 0;
+#pragma unroll
+        for (int d = 0; d < D; ++d) {
+            while (r >= nb && rem != 0u) {
+                const int ad = __builtin_amdgcn_readlane(id, __ffs(rem) - 1);
+                mask = static_cast<uint32_t>(__ballot(id == ad)) & 0xffffu;
+                rem &= ~mask;
+                h = a.table[m][ad];
+                nb = rank_blocks(h, a.max_rank);
+                r = 0;
+            }
+            ap[m][d] = bp[m][d] = nullptr;
+            if (r < nb) {
+                ap[m][d] = static_cast<const char*>(h.a) + static_cast<size_t>(r) * S * 1024 + lane * 16;
+                bp[m][d] = static_cast<const char*>(h.b) + (static_cast<size_t>(ob) * nb + r) * 512 + lane * 8;
+                who[m][d] = mask;
+                scale[m][d] = h.scale;
+                used[m] = d + 1;
+                ++r;
+            }
+        }
+    }
+
+    f32x4 acc[NM][1 + D];
+#pragma unroll
+    for (int m = 0; m < NM; ++m)
+#pragma unroll
+        for (int d = 0; d <= D; ++d) acc[m][d] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll U
+    for (int s = wave; s < S; s += W) {
+        const size_t at = static_cast<size_t>(s) * 1024;
+        Frag<XK> f;
+        f.load(x + static_cast<size_t>(s) * Frag<XK>::kTileBytes, a.x_plane);
+        u32x4 t[NM][1 + D], xt[TT];
+#pragma unroll
+        for (int m = 0; m < NM; ++m) {
+            t[m][0] = *reinterpret_cast<const u32x4*>(w[m] + at);
+#pragma unroll
+            for (int d = 0; d < D; ++d) {
+                t[m][1 + d] = u32x4{0u, 0u, 0u, 0u};
+                if (d < used[m]) t[m][1 + d] = *reinterpret_cast<const u32x4*>(ap[m][d] + at);
+            }
+        }
+        f.terms(xt);
+#pragma unroll
+        for (int m = 0; m < NM; ++m)
+#pragma unroll
+            for (int d = 0; d <= D; ++d)
+#pragma unroll
+                for (int k = TT - 1; k >= 0; --k) acc[m][d] = mma32(t[m][d], xt[k], acc[m][d]);
+    }
+#pragma unroll
+    for (int m = 0; m < NM; ++m)
+#pragma unroll
+        for (int d = 0; d <= D; ++d)
+            if (d <= used[m]) part[wave][m * (1 + D) + d][lane] = acc[m][d];
+    __syncthreads();
+    for (int p = wave; p < kTiles; p += W) {   // each sum is one wave's, written where only that wave reads
+        if (p % (1 + D) > used[NM == 1 ? 0 : p / (1 + D)]) continue;
+        f32x4 v = part[0][p][lane];
+#pragma unroll
+        for (int i = 1; i < W; ++i) v += part[i][p][lane];
+        part[0][p][lane] = v;
+    }
+    __syncthreads();
+    if (wave != 0) return;
+    f32x4 out[NM];
+#pragma unroll
+    for (int m = 0; m < NM; ++m) {
+        out[m] = part[0][m * (1 + D)][lane];
+#pragma unroll
+        for (int d = 0; d < D; ++d) {
+            if (d >= used[m]) continue;
+            f32x4 v = part[0][m * (1 + D) + 1 + d][lane] * scale[m][d];
+            const bool mine = (who[m][d] >> n) & 1u;
+            const float f[4] = {mine ? v.x : 0.0f, mine ? v.y : 0.0f, mine ? v.z : 0.0f, mine ? v.w : 0.0f};
+            uint32_t vt[VT][2];
+            split<VT, 2>(f, vt);
+            const u32x2 b = *reinterpret_cast<const u32x2*>(bp[m][d]);
+            f32x4 sum = out[m];
+#pragma unroll
+            for (int k = VT - 1; k >= 0; --k) sum = mma16(b, u32x2{vt[k][0], vt[k][1]}, sum);
+            out[m] = mine ? sum : out[m];   // (a non-finite B stays with its own tokens)
+        }
+    }
+    if constexpr (NM == 2) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) out[0][j] = silu(out[0][j]) * out[1][j];
+    }
+    if (n < B_real) store4<YK>(a, n, 16 * ob + 4 * q, out[0]);
+}
+
+// ---------------------------------------------------------------------------
+// A decode batch: the columns are split over workgroups too, so that there
+// are enough of them, and the adapters' first products run beside the large
+// one in the same launch.
+//   split launch   workgroups of W waves: first those that form v (shrink),
+//                  then those of the product.  One of these owns RB row blocks
+//                  (of NM matrices), NT tiles of 16 tokens and one part of the
+//                  columns; its waves take pairs of tiles in turn and keep
+//                  MB x NT blocks in registers, so a weight tile is read by
+//                  one wave only and nothing is staged.  The waves' sums are
+//                  added in LDS and stored as 16 x 16 blocks of fp32.
+//   finish launch  one workgroup per block: adds the parts and B v (its waves
+//                  share the parts and the rank blocks), then the epilogue.
+// ---------------------------------------------------------------------------
+constexpr int kSplitWaves = 8;
+
+struct SplitArgs {
+    f32x4* part;         // [parts][NM][token tiles][row blocks][64]
+    int parts, steps;    // column tiles per part
+    int row_groups, tok_groups;
+    int shrink_wgs, places, by_token;
+};
+
+template <int XK, int NM, int NT, int RB>
+__global__ __launch_bounds__(kSplitWaves* kWave) void proj_split_kernel(ProjArgs a, SplitArgs g) {
+    constexpr int W = kSplitWaves, TT = Frag<XK>::kTerms, MB = NM * RB, T = MB * NT;
+    constexpr int SNT = NT == 1 ? 1 : 2;
+    union Lds {
+        f32x4 part[W / 2][T][kWave];
+        ShrinkLds<SNT, 1, W> shrink;
+    };
+    __shared__ Lds l;
+    const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
+    const int n = lane & 15, q = lane >> 4;
+    const int B_real = real_tokens(a);
+    if (static_cast<int>(blockIdx.x) < g.shrink_wgs) {
+        const int pieces = a.max_rank / 16;
+        const int at = blockIdx.x % g.places, rest = blockIdx.x / g.places;
+        const int rb = rest % pieces, t_id = rest / pieces;
+        if (a.table[t_id] == nullptr || B_real <= 0) return;
+        const int ad = shrink_adapter(a, at, g.by_token, 0, B_real);
+        if (ad >= 0) shrink_block<XK, SNT, 1, W>(a, l.shrink, t_id, ad, rb, 0, B_real, 0, 1);
+        return;
+    }
+    const int id = blockIdx.x - g.shrink_wgs;
+    const int rg = id % g.row_groups, tg = id / g.row_groups % g.tok_groups, sp = id / g.row_groups / g.tok_groups;
+    const int i0 = tg * 16 * NT;
     if (i0 >= B_real) return;
-    const int ob0 = blockIdx.x * RB, blocks = a.O / 16;
-    const int S = a.H / 32;
+    const int ob0 = rg * RB, blocks = a.O / 16, S = a.H / 32;
+    const int s0 = sp * g.steps, s1 = min(s0 + g.steps, S);
 
     const char* wp[MB];
 #pragma unroll
@@ -369,14 +554,12 @@ __global__ __launch_bounds__(W* kWave) void proj_stream_kernel(ProjArgs a) {
     const char* xp[NT];
 #pragma unroll
     for (int t = 0; t < NT; ++t) xp[t] = x_row<XK>(a, min(i0 + 16 * t + n, B_real - 1), q);
-
     f32x4 acc[MB][NT];
 #pragma unroll
     for (int j = 0; j < MB; ++j)
 #pragma unroll
         for (int t = 0; t < NT; ++t) acc[j][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll U
-    for (int s = wave; s < S; s += W) {
+    auto tile = [&](int s) {
         u32x4 w[MB];
         Frag<XK> f[NT];
 #pragma unroll
@@ -392,31 +575,79 @@ __global__ __launch_bounds__(W* kWave) void proj_stream_kernel(ProjArgs a) {
 #pragma unroll
                 for (int j = 0; j < MB; ++j) acc[j][t] = mma32(w[j], x[k], acc[j][t]);
         }
+    };
+    const int pairs = (s1 - s0) / 2;
+    constexpr int kU = T * TT > 8 ? 1 : 2;
+#pragma unroll kU
+    for (int p = wave; p < pairs; p += W) {
+        tile(s0 + 2 * p);
+        tile(s0 + 2 * p + 1);
     }
-    expand<v_terms_for<YK>()>(a, i0, B_real, wave, W, acc, [&](int j) { return min(ob0 + j % RB, blocks - 1); },
-                              [&](int j) { return j / RB; });
+    if (((s1 - s0) & 1) && wave == W - 1) tile(s1 - 1);
+
+    // waves W/2 .. hand theirs to waves 0 .. W/2 - 1, whose sums all waves then add
+    if (wave >= W / 2)
 #pragma unroll
-    for (int j = 0; j < MB; ++j)
+        for (int j = 0; j < MB; ++j)
 #pragma unroll
-        for (int t = 0; t < NT; ++t) part[wave][j * NT + t][lane] = acc[j][t];
+            for (int t = 0; t < NT; ++t) l.part[wave - W / 2][j * NT + t][lane] = acc[j][t];
     __syncthreads();
-    for (int p = wave; p < RB * NT; p += W) {
-        const int r = p / NT, t = p % NT;
-        const int ob = ob0 + r, i = i0 + 16 * t + n;
-        if (ob >= blocks || i >= B_real) continue;
-        f32x4 sum[NM];
+    if (wave < W / 2)
 #pragma unroll
-        for (int m = 0; m < NM; ++m) {
-            sum[m] = part[0][m * RB * NT + p][lane];
+        for (int j = 0; j < MB; ++j)
 #pragma unroll
-            for (int w = 1; w < W; ++w) sum[m] += part[w][m * RB * NT + p][lane];
-        }
-        if constexpr (NM == 2) {
+            for (int t = 0; t < NT; ++t) {
+                f32x4& slot = l.part[wave][j * NT + t][lane];
+                slot = acc[j][t] + slot;
+            }
+    __syncthreads();
+    const int tt_all = (a.B + 15) / 16;
+    for (int p = wave; p < T; p += W) {
+        const int j = p / NT, t = p % NT, ob = ob0 + j % RB, tt = tg * NT + t;
+        if (ob >= blocks || tt >= tt_all) continue;
+        f32x4 v = l.part[0][p][lane];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) sum[0][j] = silu(sum[0][j]) * sum[1][j];
-        }
-        store4<YK>(a, i, 16 * ob + 4 * q, sum[0]);
+        for (int w = 1; w < W / 2; ++w) v += l.part[w][p][lane];
+        g.part[(((static_cast<size_t>(sp) * NM + j / RB) * tt_all + tt) * blocks + ob) * kWave + lane] = v;
     }
+}
+
+constexpr int kFinishWaves = 4;
+
+template <int YK, int NM>
+__global__ __launch_bounds__(kFinishWaves* kWave) void proj_finish_kernel(ProjArgs a, SplitArgs g) {
+    constexpr int W = kFinishWaves;
+    __shared__ f32x4 part[W][NM][kWave];
+    const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
+    const int n = lane & 15, q = lane >> 4;
+    const int ob = blockIdx.x, tt = blockIdx.y, blocks = a.O / 16, tt_all = gridDim.y;
+    const int B_real = real_tokens(a);
+    if (16 * tt >= B_real) return;
+    f32x4 acc[NM][1];
+#pragma unroll
+    for (int m = 0; m < NM; ++m) {
+        acc[m][0] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        for (int sp = wave; sp < g.parts; sp += W)
+            acc[m][0] += g.part[(((static_cast<size_t>(sp) * NM + m) * tt_all + tt) * blocks + ob) * kWave + lane];
+    }
+    expand<v_terms_for<YK>()>(a, 16 * tt, B_real, wave, W, acc, [&](int) { return ob; }, [&](int j) { return j; });
+#pragma unroll
+    for (int m = 0; m < NM; ++m) part[wave][m][lane] = acc[m][0];
+    __syncthreads();
+    const int i = 16 * tt + n;
+    if (wave != 0 || i >= B_real) return;
+    f32x4 out[NM];
+#pragma unroll
+    for (int m = 0; m < NM; ++m) {
+        out[m] = part[0][m][lane];
+#pragma unroll
+        for (int w = 1; w < W; ++w) out[m] += part[w][m][lane];
+    }
+    if constexpr (NM == 2) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) out[0][j] = silu(out[0][j]) * out[1][j];
+    }
+    store4<YK>(a, i, 16 * ob + 4 * q, out[0]);
 }
 
 // ---------------------------------------------------------------------------
@@ -540,14 +771,50 @@ __global__ __launch_bounds__(256) void planes_kernel(const f32x4* __restrict__ x
     }
 }
 
-constexpr int kStreamTokens = 128;   // up to this many: the streaming kernel
+// ---------------------------------------------------------------------------
+// Which kernels a projection takes, from its sizes alone.
+// ---------------------------------------------------------------------------
 constexpr int kRowTokens = 16;       // up to this many: fp32 rows are cut in registers
+constexpr int kSplitTokens = 256;    // up to this many: the split kernels, above the tiled one
 
-template <int XK, int YK, int NM, int NT, int W, int U>
-void launch_stream(const ProjArgs& a, hipStream_t s) {
-    proj_stream_kernel<XK, YK, NM, NT, 1, W, U>
-        <<<dim3(a.O / 16, (a.B + 16 * NT - 1) / (16 * NT)), W * kWave, 0, s>>>(a);
+enum Path { kFused, kSplit, kTiled };
+struct Plan {
+    Path path;
+    int nt, rb;          // split: token tiles and row blocks of a workgroup
+    SplitArgs split;
+    size_t part_bytes;
+};
+
+// rank_blocks: what the batch's adapters may hold together (0: no adapters).
+Plan plan_proj(int B, int H, int O, int mats, int rank_blocks) {
+    Plan p{};
+    if (B <= 16 && rank_blocks <= kFusedBlocks) {
+        p.path = kFused;
+        return p;
+    }
+    if (B > kSplitTokens) {
+        p.path = kTiled;
+        return p;
+    }
+    p.path = kSplit;
+    p.nt = B <= 16 ? 1 : (B <= 32 ? 2 : 4);
+    p.rb = (p.nt == 4 ? 4 : 2) / mats;
+    const int blocks = O / 16, S = H / 32;
+    SplitArgs& g = p.split;
+    g.row_groups = (blocks + p.rb - 1) / p.rb;
+    g.tok_groups = (B + 16 * p.nt - 1) / (16 * p.nt);
+    // two workgroups per compute unit, but at least a pair of tiles per wave
+    const int want = std::max(1, 512 / (g.row_groups * g.tok_groups));
+    const int most = std::max(1, S / (2 * kSplitWaves));
+    g.parts = std::min(want, most);
+    g.steps = (S + g.parts - 1) / g.parts;
+    g.steps += g.steps & 1;
+    g.parts = (S + g.steps - 1) / g.steps;
+    p.part_bytes = static_cast<size_t>(g.parts) * mats * ((B + 15) / 16) * blocks * 1024;
+    return p;
 }
+int rank_blocks_bound(int B, int n_adapters, int max_rank) { return std::min(B, n_adapters) * (max_rank / 16); }
+
 template <int XK, int YK, int NM, int WR, int WC, int MB, int NB>
 hipError_t launch_tile(const ProjArgs& a, hipStream_t s) {
     constexpr int kRows = 16 * WR * MB / NM, kTok = 16 * WC * NB;
@@ -556,22 +823,15 @@ hipError_t launch_tile(const ProjArgs& a, hipStream_t s) {
     return hipGetLastError();
 }
 
-template <int XK, int YK, int NM>
-hipError_t launch_proj(const ProjArgs& a, hipStream_t s) {
-    if (a.B <= 16) launch_stream<XK, YK, NM, 1, 8, 4>(a, s);
-    else if constexpr (XK != kActF32) {
-        if (a.B <= 32) launch_stream<XK, YK, NM, 2, 8, 4>(a, s);
-        else if (a.B <= kStreamTokens) launch_stream<XK, YK, NM, 4, 8 / NM, 2>(a, s);
-        else {
-            const long big = (static_cast<long>(a.O) * NM + 255) / 256 * ((a.B + 255) / 256);
-            return big >= 128 ? launch_tile<XK, YK, NM, 2, 4, 8, 4>(a, s) : launch_tile<XK, YK, NM, 2, 2, 4, 4>(a, s);
-        }
-    }
-    return hipGetLastError();
+template <int XK, int NM, int NT, int RB>
+void launch_split(const ProjArgs& a, const SplitArgs& g, hipStream_t s) {
+    const long wgs = static_cast<long>(g.row_groups) * g.tok_groups * g.parts + g.shrink_wgs;
+    proj_split_kernel<XK, NM, NT, RB><<<static_cast<unsigned>(wgs), kSplitWaves * kWave, 0, s>>>(a, g);
 }
 
-template <int XK, int NT, int RBN, int W>
-void launch_shrink_as(const ProjArgs& a, int tables, hipStream_t s) {
+template <int XK>
+void launch_shrink(const ProjArgs& a, int tables, hipStream_t s) {
+    constexpr int NT = 4, RBN = 2, W = 8;
     const int chunk = std::min(a.B, kChunk), chunks = (a.B + kChunk - 1) / kChunk;
     const int parts = (chunk + 16 * NT - 1) / (16 * NT);
     const int by_token = a.n_adapters > chunk;
@@ -579,24 +839,50 @@ void launch_shrink_as(const ProjArgs& a, int tables, hipStream_t s) {
     shrink_kernel<XK, NT, RBN, W><<<dim3(by_token ? chunk : a.n_adapters, parts * chunks, pieces * tables), W * kWave, 0,
                                     s>>>(a, parts, by_token);
 }
-template <int XK>
-void launch_shrink(const ProjArgs& a, int tables, hipStream_t s) {
-    if (a.B <= 128) launch_shrink_as<XK, 1, 1, 8>(a, tables, s);
-    else launch_shrink_as<XK, 4, 2, 8>(a, tables, s);
-}
 
-// One projection (NM = 1) or the gate/up pair (NM = 2): shrink, then the product.
-template <int NM>
-hipError_t run_proj(const ProjArgs& a, hipStream_t s) {
-    if (a.adapter != nullptr && (a.table[0] != nullptr || (NM == 2 && a.table[1] != nullptr))) {
-        if (a.x_kind == kActBf16) launch_shrink<kActBf16>(a, NM, s);
-        else if (a.x_kind == kActPlanes) launch_shrink<kActPlanes>(a, NM, s);
-        else launch_shrink<kActF32>(a, NM, s);
+// One projection (NM = 1) or the gate/up pair (NM = 2).
+template <int XK, int YK, int NM>
+hipError_t launch_proj(const ProjArgs& a, void* part, hipStream_t s) {
+    const bool lora = a.adapter != nullptr && (a.table[0] != nullptr || (NM == 2 && a.table[1] != nullptr));
+    Plan p = plan_proj(a.B, a.H, a.O, NM, a.adapter != nullptr ? rank_blocks_bound(a.B, a.n_adapters, a.max_rank) : 0);
+    if (p.path == kFused) {
+        proj_fused_kernel<XK, YK, NM, 8, 4><<<a.O / 16, 8 * kWave, 0, s>>>(a);
+        return hipGetLastError();
+    }
+    if (p.path == kSplit) {
+        SplitArgs& g = p.split;
+        g.part = static_cast<f32x4*>(part);
+        if (lora) {
+            g.by_token = a.n_adapters > a.B;
+            g.places = g.by_token ? a.B : a.n_adapters;
+            g.shrink_wgs = g.places * (a.max_rank / 16) * NM;
+        }
+        if (p.nt == 1) launch_split<XK, NM, 1, 2 / NM>(a, g, s);
+        else if constexpr (XK != kActF32) {
+            if (p.nt == 2) launch_split<XK, NM, 2, 2 / NM>(a, g, s);
+            else launch_split<XK, NM, 4, 4 / NM>(a, g, s);
+        }
         hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
+        proj_finish_kernel<YK, NM><<<dim3(a.O / 16, (a.B + 15) / 16), kFinishWaves * kWave, 0, s>>>(a, g);
+        return hipGetLastError();
     }
+    if constexpr (XK != kActF32) {
+        if (lora) {
+            launch_shrink<XK>(a, NM, s);
+            hipError_t e = hipGetLastError();
+            if (e != hipSuccess) return e;
+        }
+        const long big = (static_cast<long>(a.O) * NM + 255) / 256 * ((a.B + 255) / 256);
+        return big >= 128 ? launch_tile<XK, YK, NM, 2, 4, 8, 4>(a, s) : launch_tile<XK, YK, NM, 2, 2, 4, 4>(a, s);
+    }
+    return hipErrorInvalidValue;
+}
+
+template <int NM>
+hipError_t run_proj(const ProjArgs& a, void* part, hipStream_t s) {
 #define MOE_PROJ(X_, Y_) \
-    if (a.x_kind == X_ && a.y_kind == Y_) return launch_proj<X_, Y_, NM>(a, s)
+    if (a.x_kind == X_ && a.y_kind == Y_) return launch_proj<X_, Y_, NM>(a, part, s)
     MOE_PROJ(kActBf16, kActBf16);
     MOE_PROJ(kActF32, kActBf16);
     MOE_PROJ(kActPlanes, kActBf16);
@@ -653,6 +939,10 @@ size_t v_bytes(int B, int max_rank) { return up256(static_cast<size_t>(B) * max_
 size_t x_planes_bytes(int B, int H, int x_dtype) {   // fp32 x of more than kRowTokens tokens
     return x_dtype == MOE_DT_F32 && B > kRowTokens ? 3 * up256(static_cast<size_t>(B) * H * 2) : 0;
 }
+// Partial blocks of a projection: the most any number of adapters asks for.
+size_t part_bytes(int B, int H, int O, int mats) {
+    return up256(plan_proj(B, H, O, mats, kFusedBlocks + 1).part_bytes);
+}
 
 // Cut an fp32 x into planes at `ws` where the call's kernels read planes.
 hipError_t cut_x(ProjArgs& a, void* ws, hipStream_t s) {
@@ -669,20 +959,26 @@ hipError_t cut_x(ProjArgs& a, void* ws, hipStream_t s) {
 
 }  // namespace
 
-size_t lora_workspace_bytes(int B, int H, int max_rank, int x_dtype) {
-    return v_bytes(B, max_rank) + x_planes_bytes(B, H, x_dtype);
+// v, the planes of x, partial blocks.
+size_t lora_workspace_bytes(int B, int H, int O, int max_rank, int x_dtype) {
+    return v_bytes(B, max_rank) + x_planes_bytes(B, H, x_dtype) + part_bytes(B, H, O, 1);
 }
 
-// v of gate, up and down, the planes of x, h (bf16, or three planes for an fp32 y).
+// v of gate, up and down, the planes of x, h (bf16, or three planes for an
+// fp32 y), partial blocks of the larger projection.
 size_t shared_ffn_workspace_bytes(int B, int H, int I, int max_rank, int x_dtype, int y_dtype) {
     return 3 * v_bytes(B, max_rank) + x_planes_bytes(B, H, x_dtype) +
-           (y_dtype == MOE_DT_F32 ? 3 : 1) * up256(static_cast<size_t>(B) * I * 2);
+           (y_dtype == MOE_DT_F32 ? 3 : 1) * up256(static_cast<size_t>(B) * I * 2) +
+           std::max(part_bytes(B, H, I, 2), part_bytes(B, I, H, 1));
 }
 
 hipError_t launch_lora_linear(ProjArgs a, void* ws, hipStream_t s) {
+    char* p = static_cast<char*>(ws);
     a.v[0] = static_cast<float*>(ws);
-    hipError_t e = cut_x(a, static_cast<char*>(ws) + v_bytes(a.B, a.max_rank), s);
-    return e != hipSuccess ? e : run_proj<1>(a, s);
+    char* planes = p + v_bytes(a.B, a.max_rank);
+    char* part = planes + x_planes_bytes(a.B, a.H, a.x_kind == kActF32 ? MOE_DT_F32 : MOE_DT_BF16);
+    hipError_t e = cut_x(a, planes, s);
+    return e != hipSuccess ? e : run_proj<1>(a, part, s);
 }
 
 hipError_t launch_shared_ffn(ProjArgs a, const void* w_down, const moe_lora_handle* t_down, void* ws, hipStream_t s) {
@@ -707,9 +1003,10 @@ hipError_t launch_shared_ffn(ProjArgs a, const void* w_down, const moe_lora_hand
     d.x_plane = h_plane;
     d.H = a.O;
     d.O = a.H;
+    char* part = h + (a.y_kind == kActPlanes ? 3 : 1) * h_plane;
     hipError_t e = cut_x(a, x_planes, s);
-    if (e == hipSuccess) e = run_proj<2>(a, s);
-    return e != hipSuccess ? e : run_proj<1>(d, s);
+    if (e == hipSuccess) e = run_proj<2>(a, part, s);
+    return e != hipSuccess ? e : run_proj<1>(d, part, s);
 }
 
 hipError_t launch_lora_pack(const uint16_t* a, const uint16_t* b, int rank, int H, int O, void* dst_a, void* dst_b,

@@ -75,7 +75,9 @@ LINEAR = [   # B, H, O, adapters, ranks, runs
     (64, 2048, 256, 24, (8, 16, 32, 64), False), (65, 96, 48, 30, (256,), False), (100, 352, 112, 6, (24,), True),
     (128, 1024, 768, 16, (16, 48), False), (129, 64, 272, 3, (7,), True), (200, 416, 400, 1, (32,), False),
     (257, 544, 144, 12, (9, 31), False), (300, 2048, 2064, 4, (16, 64), True), (515, 1120, 656, 8, (12,), False),
-    (1025, 288, 528, 5, (40, 16), True), (1, 8192, 64, 1, (64,), True),
+    (1025, 288, 528, 5, (40, 16), True), (1, 8192, 64, 1, (64,), True), (4, 96, 64, 9, (16,), False),
+    (2, 1056, 32, 5, (32, 5), False), (3, 32, 48, 1, (50,), False), (13, 64, 32, 2, (20,), False),
+    (256, 160, 96, 300, (3, 18), False), (2500, 64, 48, 2600, (5,), False), (2100, 96, 64, 3, (20,), False),
 ]
 
 
@@ -123,25 +125,27 @@ def test_accumulate_and_padding_rows(B):
             _check_linear(y[:m], x[:m], W, entries, ids[:m], "f32")
 
 
-@pytest.mark.parametrize("B", [5, 48, 160, 300])
+@pytest.mark.parametrize("B", [5, 20, 48, 160, 300])
 @pytest.mark.parametrize("xdt", ["bf16", "f32"])
 def test_non_finite_values_stay_in_their_rows(B, xdt):
     H, O, n = 128, 96, 5
     entries = lora_ref.make_table(17, n, H, O, (16, 20))
     entries[3] = (torch.full_like(entries[3][0], float("inf")), entries[3][1], 1.0)   # used by no token
+    entries[4] = (entries[4][0], torch.full_like(entries[4][1], float("nan")), 1.0)
     W, x, ids = _weights(18, O, H), _acts(19, B, H, xdt), _ids(20, B, n)
-    ids[ids == 3] = 1
+    ids[ids >= 3] = 1
     t, w = _table(entries, H, O), _pack(W)
     clean = moe.lora_linear(x.to(DEV), w, t, ids.to(DEV), y_dtype=torch.float32)
     _check_linear(clean, x, W, entries, ids, "f32")
     bad = x.clone()
     bad[1, 3], bad[2, 5] = float("nan"), float("inf")
     ids2 = ids.clone()
-    ids2[4] = 3                            # one token takes the adapter of infinities
+    ids2[4], ids2[3] = 3, 4                # one token takes the adapter of infinities, one that of NaN
     y = moe.lora_linear(bad.to(DEV), w, t, ids2.to(DEV), y_dtype=torch.float32)
-    rows = [i for i in range(B) if i not in (1, 2, 4)]
+    rows = [i for i in range(B) if i not in (1, 2, 3, 4)]
     assert torch.equal(y[rows], clean[rows])
     assert torch.isnan(y[1]).all() and not torch.isfinite(y[2]).any() and not torch.isfinite(y[4]).any()
+    assert torch.isnan(y[3]).all()
 
 
 @pytest.mark.parametrize("B", [9, 64, 129, 320])
