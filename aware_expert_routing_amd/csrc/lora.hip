@@ -20,6 +20,7 @@
 #include "internal.h"
 
 #include <algorithm>
+#include <cstdlib>
 
 namespace moe {
 namespace {
@@ -141,58 +142,79 @@ __device__ __forceinline__ int rank_blocks(const moe_lora_handle& h, int max_ran
 // of A; its W waves take pairs of the columns' tiles in turn (a pair is one
 // 128-byte line of a bf16 row) and add their sums in LDS in a fixed order.
 // ---------------------------------------------------------------------------
+constexpr int kChunk = 2048;
+
 template <int NT, int RBN, int W>
 struct ShrinkLds {
-    f32x4 part[W][RBN * NT][kWave];
+    f32x4 part[W / 2][RBN * NT][kWave];
     int tok[16 * NT];
-    int wave_n[W];
+    int found[kChunk / kWave];
 };
 
+// Adds the W waves' accumulator blocks (T of them, in order wave, wave + W/2)
+// pairwise into part[0 .. W/2 - 1]; the caller's threads are synchronised after.
+template <int W, int T>
+__device__ __forceinline__ void fold_waves(f32x4 (*part)[T][kWave], const f32x4 (&acc)[T], int wave, int lane) {
+    if (wave >= W / 2)
+#pragma unroll
+        for (int p = 0; p < T; ++p) part[wave - W / 2][p][lane] = acc[p];
+    __syncthreads();
+    if (wave < W / 2)
+#pragma unroll
+        for (int p = 0; p < T; ++p) part[wave][p][lane] = acc[p] + part[wave][p][lane];
+    __syncthreads();
+}
+
 // Parts first_part, first_part + step, .. (step 0: that part alone) of adapter
-// ad's tokens, rank blocks rb0 .. of table t_id.
+// ad's tokens, rank blocks rb0 .. of table t_id; c1 - c0 <= kChunk.
 template <int XK, int NT, int RBN, int W>
 __device__ __forceinline__ void shrink_block(const ProjArgs& a, ShrinkLds<NT, RBN, W>& l, int t_id, int ad, int rb0,
                                              int c0, int c1, int first_part, int step) {
+    constexpr int U = kChunk / (W * kWave);   // ids a thread looks at
     const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
     const int n = lane & 15, q = lane >> 4;
     const moe_lora_handle h = a.table[t_id][ad];
     const int nb = rank_blocks(h, a.max_rank);
     if (rb0 >= nb) return;
+    // the chunk's tokens of this adapter: their number, and this thread's places among them
+    int at[U];
+    uint64_t b[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int i = c0 + u * W * kWave + tid;
+        b[u] = __ballot(i < c1 && a.adapter[i] == ad);
+        if (lane == 0) l.found[u * W + wave] = __popcll(b[u]);
+    }
+    __syncthreads();
+    int all = 0;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        at[u] = all + __popcll(b[u] & ((1ull << lane) - 1ull));
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+            const int f = l.found[u * W + w];
+            at[u] += w < wave ? f : 0;
+            all += f;
+        }
+    }
     const int S = a.H / 32;
     const char* A[RBN];
 #pragma unroll
     for (int r = 0; r < RBN; ++r)
         A[r] = static_cast<const char*>(h.a) + static_cast<size_t>(min(rb0 + r, nb - 1)) * S * 1024 + lane * 16;
-    for (int part_id = first_part;; part_id += step) {
-        // the chunk's tokens of this adapter, in order: places part_id 16 NT ..
-        int base = -part_id * 16 * NT;   // place of the next match, relative to this part
-        for (int i0 = c0; i0 < c1; i0 += W * kWave) {
-            const int i = i0 + tid;
-            const bool m = i < c1 && a.adapter[i] == ad;
-            const uint64_t b = __ballot(m);
-            if (lane == 0) l.wave_n[wave] = __popcll(b);
-            __syncthreads();
-            int at = base + __popcll(b & ((1ull << lane) - 1ull));
+    for (int base = first_part * 16 * NT; base < all; base += step * 16 * NT) {
+        const int have = min(all - base, 16 * NT);
 #pragma unroll
-            for (int w = 0; w < W; ++w) {
-                at += w < wave ? l.wave_n[w] : 0;
-                base += l.wave_n[w];
-            }
-            if (m && at >= 0 && at < 16 * NT) l.tok[at] = i;
-            __syncthreads();
-            if (base > 16 * NT) break;
-        }
-        const int have = min(base, 16 * NT);
-        if (have <= 0) return;
-
+        for (int u = 0; u < U; ++u)
+            if (((b[u] >> lane) & 1ull) && at[u] >= base && at[u] < base + 16 * NT)
+                l.tok[at[u] - base] = c0 + u * W * kWave + tid;
+        __syncthreads();
         const char* xp[NT];
 #pragma unroll
         for (int t = 0; t < NT; ++t) xp[t] = x_row<XK>(a, l.tok[min(16 * t + n, have - 1)], q);
-        f32x4 acc[RBN][NT];
+        f32x4 acc[RBN * NT];
 #pragma unroll
-        for (int r = 0; r < RBN; ++r)
-#pragma unroll
-            for (int t = 0; t < NT; ++t) acc[r][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        for (int p = 0; p < RBN * NT; ++p) acc[p] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
         auto tile = [&](int s) {
             u32x4 w[RBN];
 #pragma unroll
@@ -207,10 +229,12 @@ __device__ __forceinline__ void shrink_block(const ProjArgs& a, ShrinkLds<NT, RB
 #pragma unroll
                 for (int k = Frag<XK>::kTerms - 1; k >= 0; --k)
 #pragma unroll
-                    for (int r = 0; r < RBN; ++r) acc[r][t] = mma32(w[r], x[k], acc[r][t]);
+                    for (int r = 0; r < RBN; ++r) acc[r * NT + t] = mma32(w[r], x[k], acc[r * NT + t]);
             }
         };
-        constexpr int kU = Frag<XK>::kTerms > 1 || RBN * NT > 4 ? 1 : 2;
+        // about 24 loads of a wave in flight
+        constexpr int kLoads = 2 * (RBN + NT * (XK == kActF32 ? 2 : Frag<XK>::kTerms));
+        constexpr int kU = kLoads >= 12 ? 1 : (kLoads > 6 ? 2 : 4);
         const int pairs = S / 2;
 #pragma unroll kU
         for (int s = wave; s < pairs; s += W) {
@@ -218,21 +242,17 @@ __device__ __forceinline__ void shrink_block(const ProjArgs& a, ShrinkLds<NT, RB
             tile(2 * s + 1);
         }
         if ((S & 1) && wave == W - 1) tile(S - 1);
-#pragma unroll
-        for (int r = 0; r < RBN; ++r)
-#pragma unroll
-            for (int t = 0; t < NT; ++t) l.part[wave][r * NT + t][lane] = acc[r][t];
-        __syncthreads();
+        fold_waves<W>(l.part, acc, wave, lane);
         for (int p = wave; p < RBN * NT; p += W) {
             const int r = p / NT, t = p % NT;
             if (rb0 + r >= nb || 16 * t + n >= have) continue;
             f32x4 v = l.part[0][p][lane];
 #pragma unroll
-            for (int w = 1; w < W; ++w) v += l.part[w][p][lane];
+            for (int w = 1; w < W / 2; ++w) v += l.part[w][p][lane];
             float* out = a.v[t_id] + static_cast<size_t>(l.tok[16 * t + n]) * a.max_rank + 16 * (rb0 + r) + 4 * q;
             *reinterpret_cast<f32x4*>(out) = v * h.scale;
         }
-        if (step == 0 || base <= 16 * NT) return;
+        if (step == 0) return;
         __syncthreads();
     }
 }
@@ -250,8 +270,6 @@ __device__ __forceinline__ int shrink_adapter(const ProjArgs& a, int at, int by_
     for (int i = c0 + static_cast<int>(threadIdx.x); i < c0 + at; i += blockDim.x) dup |= a.adapter[i] == ad;
     return __syncthreads_or(dup) ? -1 : ad;
 }
-
-constexpr int kChunk = 2048;
 
 // grid: (places, parts x chunks, pieces of rank blocks x tables)
 template <int XK, int NT, int RBN, int W>
@@ -278,13 +296,11 @@ __device__ __forceinline__ void v_terms(const float* v_row, int r, int q, bool m
 }
 
 // Adds B_a v to the accumulators of MB row blocks and NB tiles of 16 tokens
-// (i0 the first token), one adapter of those tokens after the other.  Of
-// adapter d's rank blocks r those with (d + r) mod step == first (step a power
-// of two): which wave adds a token's part does not depend on the other
-// tokens.  ob(j): row block of accumulator row j, mat(j): its matrix.
+// (i0 the first token), one adapter of those tokens after the other.  ob(j):
+// row block of accumulator row j, mat(j): its matrix.
 template <int VT, int MB, int NB, typename Ob, typename Mat>
-__device__ __forceinline__ void expand(const ProjArgs& a, int i0, int B_real, int first, int step,
-                                       f32x4 (&acc)[MB][NB], Ob ob, Mat mat) {
+__device__ __forceinline__ void expand(const ProjArgs& a, int i0, int B_real, f32x4 (&acc)[MB][NB], Ob ob,
+                                       Mat mat) {
     static_assert(NB <= 4, "a token per lane");
     if (a.adapter == nullptr) return;
     const int lane = threadIdx.x & (kWave - 1), n = lane & 15, q = lane >> 4;
@@ -304,7 +320,7 @@ __device__ __forceinline__ void expand(const ProjArgs& a, int i0, int B_real, in
                 nb[m] = rank_blocks(h[m], a.max_rank);
             }
         const int most = max(nb[0], nb[1]);
-        for (int r = (first - ad) & (step - 1); r < most; r += step) {
+        for (int r = 0; r < most; ++r) {
             u32x2 b[MB];
 #pragma unroll
             for (int j = 0; j < MB; ++j) {
@@ -505,18 +521,70 @@ __global__ __launch_bounds__(W* kWave) void proj_fused_kernel(ProjArgs a) {
 //                  columns; its waves take pairs of tiles in turn and keep
 //                  MB x NT blocks in registers, so a weight tile is read by
 //                  one wave only and nothing is staged.  The waves' sums are
-//                  added in LDS and stored as 16 x 16 blocks of fp32.
-//   finish launch  one workgroup per block: adds the parts and B v (its waves
-//                  share the parts and the rank blocks), then the epilogue.
+//                  added in LDS and stored as 16 x 16 blocks of fp32.  Some
+//                  workgroups list, for each tile of 16 tokens, the rank
+//                  blocks of B its adapters bring, so that the finish launch
+//                  reads the list in place of forming it once per row block.
+//   finish launch  a workgroup per few row blocks and token tile: adds the
+//                  parts and B v (its waves share both), then the epilogue.
 // ---------------------------------------------------------------------------
 constexpr int kSplitWaves = 8;
+constexpr int kFinishWaves = 8;
+
+// A rank block of one adapter among the tokens of a tile.
+struct RankItem {
+    const char* b;   // its half tile of row block 0; row block ob lies ob * nb * 512 further
+    uint32_t who;    // the adapter's tokens in the tile
+    uint16_t nb, r;
+};
+// An adapter's rank block r is wave (adapter + r) mod kFinishWaves' item, so
+// that which wave adds a token's part does not depend on the other tokens: at
+// most two of an adapter's 16 rank blocks, for 16 adapters.
+constexpr int kMaxItems = 16 * (kMaxLoraRank / 16 / kFinishWaves);
 
 struct SplitArgs {
     f32x4* part;         // [parts][NM][token tiles][row blocks][64]
+    RankItem* items;     // [NM][token tiles][kFinishWaves][kMaxItems]
+    int* n_items;        // [NM][token tiles][kFinishWaves]
     int parts, steps;    // column tiles per part
     int row_groups, tok_groups;
     int shrink_wgs, places, by_token;
+    int list_wgs;        // one per matrix and token tile, 0: no adapters
 };
+
+// The calling wave's list for matrix m and token tile tt.
+__device__ __forceinline__ void list_items(const ProjArgs& a, const SplitArgs& g, int m, int tt, int tt_all, int wave,
+                                           int B_real) {
+    const int lane = threadIdx.x & (kWave - 1);
+    const int id = adapter_of(a, 16 * tt + (lane & 15), B_real);
+    const size_t at = (static_cast<size_t>(m) * tt_all + tt) * kFinishWaves + wave;
+    int nb = 0, count = 0;
+    uint64_t base = 0;
+    if (a.table[m] != nullptr && id >= 0) {   // every lane reads its own token's handle, all in one round trip
+        const moe_lora_handle* h = a.table[m] + id;
+        nb = rank_blocks(*h, a.max_rank);
+        base = reinterpret_cast<uint64_t>(h->b);
+    }
+    uint32_t rem = static_cast<uint32_t>(__ballot(nb > 0)) & 0xffffu;
+    while (rem != 0u) {
+        const int from = __ffs(rem) - 1;
+        const int ad = __builtin_amdgcn_readlane(id, from);
+        const uint32_t who = static_cast<uint32_t>(__ballot(id == ad)) & 0xffffu;
+        rem &= ~who;
+        const int n = __builtin_amdgcn_readlane(nb, from);
+        const uint64_t b =
+            (static_cast<uint64_t>(static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(base >> 32), from)))
+             << 32) |
+            static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(base), from));
+        for (int r = (wave - ad) & (kFinishWaves - 1); r < n; r += kFinishWaves) {
+            if (lane == 0)
+                g.items[at * kMaxItems + count] = RankItem{reinterpret_cast<const char*>(b) + r * 512, who,
+                                                           static_cast<uint16_t>(n), static_cast<uint16_t>(r)};
+            ++count;
+        }
+    }
+    if (lane == 0) g.n_items[at] = count;
+}
 
 template <int XK, int NM, int NT, int RB>
 __global__ __launch_bounds__(kSplitWaves* kWave) void proj_split_kernel(ProjArgs a, SplitArgs g) {
@@ -539,7 +607,12 @@ __global__ __launch_bounds__(kSplitWaves* kWave) void proj_split_kernel(ProjArgs
         if (ad >= 0) shrink_block<XK, SNT, 1, W>(a, l.shrink, t_id, ad, rb, 0, B_real, 0, 1);
         return;
     }
-    const int id = blockIdx.x - g.shrink_wgs;
+    if (static_cast<int>(blockIdx.x) < g.shrink_wgs + g.list_wgs) {
+        const int at = blockIdx.x - g.shrink_wgs, tt_all = (a.B + 15) / 16;
+        if (16 * (at % tt_all) < B_real) list_items(a, g, at / tt_all, at % tt_all, tt_all, wave, B_real);
+        return;
+    }
+    const int id = blockIdx.x - g.shrink_wgs - g.list_wgs;
     const int rg = id % g.row_groups, tg = id / g.row_groups % g.tok_groups, sp = id / g.row_groups / g.tok_groups;
     const int i0 = tg * 16 * NT;
     if (i0 >= B_real) return;
@@ -554,11 +627,9 @@ __global__ __launch_bounds__(kSplitWaves* kWave) void proj_split_kernel(ProjArgs
     const char* xp[NT];
 #pragma unroll
     for (int t = 0; t < NT; ++t) xp[t] = x_row<XK>(a, min(i0 + 16 * t + n, B_real - 1), q);
-    f32x4 acc[MB][NT];
+    f32x4 acc[T];   // block j NT + t
 #pragma unroll
-    for (int j = 0; j < MB; ++j)
-#pragma unroll
-        for (int t = 0; t < NT; ++t) acc[j][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int p = 0; p < T; ++p) acc[p] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     auto tile = [&](int s) {
         u32x4 w[MB];
         Frag<XK> f[NT];
@@ -573,34 +644,22 @@ __global__ __launch_bounds__(kSplitWaves* kWave) void proj_split_kernel(ProjArgs
 #pragma unroll
             for (int k = TT - 1; k >= 0; --k)
 #pragma unroll
-                for (int j = 0; j < MB; ++j) acc[j][t] = mma32(w[j], x[k], acc[j][t]);
+                for (int j = 0; j < MB; ++j) acc[j * NT + t] = mma32(w[j], x[k], acc[j * NT + t]);
         }
     };
-    const int pairs = (s1 - s0) / 2;
-    constexpr int kU = T * TT > 8 ? 1 : 2;
+    if (s1 - s0 >= 2 * W) {   // pairs of tiles: one 128-byte line of a bf16 row
+        const int pairs = (s1 - s0) / 2;
+        constexpr int kU = T * TT > 8 ? 1 : 2;
 #pragma unroll kU
-    for (int p = wave; p < pairs; p += W) {
-        tile(s0 + 2 * p);
-        tile(s0 + 2 * p + 1);
+        for (int p = wave; p < pairs; p += W) {
+            tile(s0 + 2 * p);
+            tile(s0 + 2 * p + 1);
+        }
+        if (((s1 - s0) & 1) && wave == W - 1) tile(s1 - 1);
+    } else {                  // fewer: a tile for every wave first
+        for (int s = s0 + wave; s < s1; s += W) tile(s);
     }
-    if (((s1 - s0) & 1) && wave == W - 1) tile(s1 - 1);
-
-    // waves W/2 .. hand theirs to waves 0 .. W/2 - 1, whose sums all waves then add
-    if (wave >= W / 2)
-#pragma unroll
-        for (int j = 0; j < MB; ++j)
-#pragma unroll
-            for (int t = 0; t < NT; ++t) l.part[wave - W / 2][j * NT + t][lane] = acc[j][t];
-    __syncthreads();
-    if (wave < W / 2)
-#pragma unroll
-        for (int j = 0; j < MB; ++j)
-#pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                f32x4& slot = l.part[wave][j * NT + t][lane];
-                slot = acc[j][t] + slot;
-            }
-    __syncthreads();
+    fold_waves<W>(l.part, acc, wave, lane);
     const int tt_all = (a.B + 15) / 16;
     for (int p = wave; p < T; p += W) {
         const int j = p / NT, t = p % NT, ob = ob0 + j % RB, tt = tg * NT + t;
@@ -612,36 +671,85 @@ __global__ __launch_bounds__(kSplitWaves* kWave) void proj_split_kernel(ProjArgs
     }
 }
 
-constexpr int kFinishWaves = 4;
-
-template <int YK, int NM>
+// A workgroup: RBF row blocks (of NM matrices) and one tile of 16 tokens.
+template <int YK, int NM, int RBF>
 __global__ __launch_bounds__(kFinishWaves* kWave) void proj_finish_kernel(ProjArgs a, SplitArgs g) {
-    constexpr int W = kFinishWaves;
-    __shared__ f32x4 part[W][NM][kWave];
+    constexpr int W = kFinishWaves, VT = v_terms_for<YK>(), T = NM * RBF;
+    constexpr int D = 2;   // rank blocks in flight per matrix
+    __shared__ f32x4 part[W / 2][T][kWave];
     const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
     const int n = lane & 15, q = lane >> 4;
-    const int ob = blockIdx.x, tt = blockIdx.y, blocks = a.O / 16, tt_all = gridDim.y;
+    const int tt = blockIdx.y, blocks = a.O / 16, tt_all = gridDim.y, ob0 = blockIdx.x * RBF;
     const int B_real = real_tokens(a);
     if (16 * tt >= B_real) return;
-    f32x4 acc[NM][1];
-#pragma unroll
-    for (int m = 0; m < NM; ++m) {
-        acc[m][0] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-        for (int sp = wave; sp < g.parts; sp += W)
-            acc[m][0] += g.part[(((static_cast<size_t>(sp) * NM + m) * tt_all + tt) * blocks + ob) * kWave + lane];
-    }
-    expand<v_terms_for<YK>()>(a, 16 * tt, B_real, wave, W, acc, [&](int) { return ob; }, [&](int j) { return j; });
-#pragma unroll
-    for (int m = 0; m < NM; ++m) part[wave][m][lane] = acc[m][0];
-    __syncthreads();
     const int i = 16 * tt + n;
-    if (wave != 0 || i >= B_real) return;
+    f32x4 acc[T];   // block m RBF + j
+#pragma unroll
+    for (int p = 0; p < T; ++p) acc[p] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int sp = wave; sp < g.parts; sp += W)
+#pragma unroll
+        for (int p = 0; p < T; ++p)
+            acc[p] += g.part[(((static_cast<size_t>(sp) * NM + p / RBF) * tt_all + tt) * blocks +
+                              min(ob0 + p % RBF, blocks - 1)) * kWave + lane];
+    if (g.list_wgs > 0) {
+        const size_t row = static_cast<size_t>(min(i, B_real - 1)) * a.max_rank;
+        const RankItem* items[NM];
+        int count[NM], most = 0;
+#pragma unroll
+        for (int m = 0; m < NM; ++m) {
+            const size_t at = (static_cast<size_t>(m) * tt_all + tt) * W + __builtin_amdgcn_readfirstlane(wave);
+            items[m] = g.items + at * kMaxItems;
+            count[m] = g.n_items[at];
+            most = max(most, count[m]);
+        }
+        for (int d0 = 0; d0 < most; d0 += D) {   // D items of each matrix, whose loads are in flight together
+            u32x2 b[NM][D][RBF];
+            f32x4 v[NM][D];
+            uint32_t who[NM][D];
+#pragma unroll
+            for (int m = 0; m < NM; ++m)
+#pragma unroll
+                for (int d = 0; d < D; ++d) {
+                    who[m][d] = 0u;
+                    if (d0 + d >= count[m]) continue;
+                    const RankItem it = items[m][d0 + d];
+                    who[m][d] = it.who;
+#pragma unroll
+                    for (int j = 0; j < RBF; ++j)
+                        b[m][d][j] = *reinterpret_cast<const u32x2*>(
+                            it.b + static_cast<size_t>(min(ob0 + j, blocks - 1)) * it.nb * 512 + lane * 8);
+                    v[m][d] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+                    if ((it.who >> n) & 1u)
+                        v[m][d] = *reinterpret_cast<const f32x4*>(a.v[m] + row + 16 * it.r + 4 * q);
+                }
+#pragma unroll
+            for (int m = 0; m < NM; ++m)
+#pragma unroll
+                for (int d = 0; d < D; ++d) {
+                    if (who[m][d] == 0u) continue;
+                    const bool mine = (who[m][d] >> n) & 1u;
+                    const float f[4] = {v[m][d].x, v[m][d].y, v[m][d].z, v[m][d].w};
+                    uint32_t t[VT][2];
+                    split<VT, 2>(f, t);
+#pragma unroll
+                    for (int j = 0; j < RBF; ++j) {
+                        f32x4 sum = acc[m * RBF + j];
+#pragma unroll
+                        for (int k = VT - 1; k >= 0; --k) sum = mma16(b[m][d][j], u32x2{t[k][0], t[k][1]}, sum);
+                        acc[m * RBF + j] = mine ? sum : acc[m * RBF + j];   // (a non-finite B stays with its own tokens)
+                    }
+                }
+        }
+    }
+    fold_waves<W>(part, acc, wave, lane);
+    const int ob = ob0 + wave;
+    if (wave >= RBF || ob >= blocks || i >= B_real) return;
     f32x4 out[NM];
 #pragma unroll
     for (int m = 0; m < NM; ++m) {
-        out[m] = part[0][m][lane];
+        out[m] = part[0][m * RBF + wave][lane];
 #pragma unroll
-        for (int w = 1; w < W; ++w) out[m] += part[w][m][lane];
+        for (int w = 1; w < W / 2; ++w) out[m] += part[w][m * RBF + wave][lane];
     }
     if constexpr (NM == 2) {
 #pragma unroll
@@ -738,7 +846,7 @@ __global__ __launch_bounds__(WR* WC* kWave) void proj_tile_kernel(ProjArgs a, in
     }
     multiply((its - 1) & 1, 0);
     if ((steps & 1) == 0) multiply((its - 1) & 1, 1);
-    expand<v_terms_for<YK>()>(a, i0 + 16 * NB * wc, B_real, 0, 1, acc,
+    expand<v_terms_for<YK>()>(a, i0 + 16 * NB * wc, B_real, acc,
                               [&](int j) { return ob_of(wr * MB + j); }, [&](int j) { return mat_of(j); });
 #pragma unroll
     for (int j = 0; j < kHalf; ++j) {
@@ -782,7 +890,7 @@ struct Plan {
     Path path;
     int nt, rb;          // split: token tiles and row blocks of a workgroup
     SplitArgs split;
-    size_t part_bytes;
+    size_t part_bytes, item_bytes, count_bytes;
 };
 
 // rank_blocks: what the batch's adapters may hold together (0: no adapters).
@@ -798,19 +906,22 @@ Plan plan_proj(int B, int H, int O, int mats, int rank_blocks) {
     }
     p.path = kSplit;
     p.nt = B <= 16 ? 1 : (B <= 32 ? 2 : 4);
-    p.rb = (p.nt == 4 ? 4 : 2) / mats;
+    p.rb = (p.nt == 4 ? 4 : 2) / mats;   // (as the instances in launch_proj)
     const int blocks = O / 16, S = H / 32;
     SplitArgs& g = p.split;
     g.row_groups = (blocks + p.rb - 1) / p.rb;
     g.tok_groups = (B + 16 * p.nt - 1) / (16 * p.nt);
     // two workgroups per compute unit, but at least a pair of tiles per wave
-    const int want = std::max(1, 512 / (g.row_groups * g.tok_groups));
+    const int want = std::max(1, (getenv("KW") ? atoi(getenv("KW")) : 512) / (g.row_groups * g.tok_groups));
     const int most = std::max(1, S / (2 * kSplitWaves));
     g.parts = std::min(want, most);
     g.steps = (S + g.parts - 1) / g.parts;
     g.steps += g.steps & 1;
     g.parts = (S + g.steps - 1) / g.steps;
+    const size_t lists = static_cast<size_t>(mats) * ((B + 15) / 16) * kFinishWaves;
     p.part_bytes = static_cast<size_t>(g.parts) * mats * ((B + 15) / 16) * blocks * 1024;
+    p.item_bytes = lists * kMaxItems * sizeof(RankItem);
+    p.count_bytes = lists * sizeof(int);
     return p;
 }
 int rank_blocks_bound(int B, int n_adapters, int max_rank) { return std::min(B, n_adapters) * (max_rank / 16); }
@@ -825,13 +936,13 @@ hipError_t launch_tile(const ProjArgs& a, hipStream_t s) {
 
 template <int XK, int NM, int NT, int RB>
 void launch_split(const ProjArgs& a, const SplitArgs& g, hipStream_t s) {
-    const long wgs = static_cast<long>(g.row_groups) * g.tok_groups * g.parts + g.shrink_wgs;
+    const long wgs = static_cast<long>(g.row_groups) * g.tok_groups * g.parts + g.shrink_wgs + g.list_wgs;
     proj_split_kernel<XK, NM, NT, RB><<<static_cast<unsigned>(wgs), kSplitWaves * kWave, 0, s>>>(a, g);
 }
 
 template <int XK>
 void launch_shrink(const ProjArgs& a, int tables, hipStream_t s) {
-    constexpr int NT = 4, RBN = 2, W = 8;
+    constexpr int NT = 2, RBN = 4, W = 16;
     const int chunk = std::min(a.B, kChunk), chunks = (a.B + kChunk - 1) / kChunk;
     const int parts = (chunk + 16 * NT - 1) / (16 * NT);
     const int by_token = a.n_adapters > chunk;
@@ -851,11 +962,15 @@ hipError_t launch_proj(const ProjArgs& a, void* part, hipStream_t s) {
     }
     if (p.path == kSplit) {
         SplitArgs& g = p.split;
+        char* lists = static_cast<char*>(part) + p.part_bytes;
         g.part = static_cast<f32x4*>(part);
+        g.items = reinterpret_cast<RankItem*>(lists);
+        g.n_items = reinterpret_cast<int*>(lists + p.item_bytes);
         if (lora) {
             g.by_token = a.n_adapters > a.B;
             g.places = g.by_token ? a.B : a.n_adapters;
             g.shrink_wgs = g.places * (a.max_rank / 16) * NM;
+            g.list_wgs = NM * ((a.B + 15) / 16);
         }
         if (p.nt == 1) launch_split<XK, NM, 1, 2 / NM>(a, g, s);
         else if constexpr (XK != kActF32) {
@@ -864,7 +979,11 @@ hipError_t launch_proj(const ProjArgs& a, void* part, hipStream_t s) {
         }
         hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
-        proj_finish_kernel<YK, NM><<<dim3(a.O / 16, (a.B + 15) / 16), kFinishWaves * kWave, 0, s>>>(a, g);
+        const int blocks = a.O / 16, tts = (a.B + 15) / 16;
+        if (blocks * tts >= 512)
+            proj_finish_kernel<YK, NM, 4><<<dim3((blocks + 3) / 4, tts), kFinishWaves * kWave, 0, s>>>(a, g);
+        else
+            proj_finish_kernel<YK, NM, 1><<<dim3(blocks, tts), kFinishWaves * kWave, 0, s>>>(a, g);
         return hipGetLastError();
     }
     if constexpr (XK != kActF32) {
@@ -939,9 +1058,11 @@ size_t v_bytes(int B, int max_rank) { return up256(static_cast<size_t>(B) * max_
 size_t x_planes_bytes(int B, int H, int x_dtype) {   // fp32 x of more than kRowTokens tokens
     return x_dtype == MOE_DT_F32 && B > kRowTokens ? 3 * up256(static_cast<size_t>(B) * H * 2) : 0;
 }
-// Partial blocks of a projection: the most any number of adapters asks for.
+// Partial blocks and item lists of a projection: the most any number of
+// adapters asks for.
 size_t part_bytes(int B, int H, int O, int mats) {
-    return up256(plan_proj(B, H, O, mats, kFusedBlocks + 1).part_bytes);
+    const Plan p = plan_proj(B, H, O, mats, kFusedBlocks + 1);
+    return up256(p.part_bytes + p.item_bytes + p.count_bytes);
 }
 
 // Cut an fp32 x into planes at `ws` where the call's kernels read planes.
