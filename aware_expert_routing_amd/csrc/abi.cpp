@@ -214,9 +214,7 @@ MOE_API int moe_route_grouped_dispatch(const void* logits, int logits_dtype, con
     int st = check_grouped(a, score, group_score, moe::kMaxExperts, moe::kMaxTopK, moe::kMaxBatch);
     if (st) return st;
     a.cnt = cnt; a.offsets = offsets; a.perm = perm; a.active = active; a.T = T; a.sync = sync;
-    hipError_t e = moe::launch_route_grouped(a, as_stream(stream));
-    if (e == hipSuccess) e = moe::launch_dispatch(idx, B, N, k, cnt, offsets, perm, active, T, as_stream(stream));
-    return hip_status(e, "moe_route_grouped_dispatch");
+    return hip_status(moe::launch_route_grouped(a, as_stream(stream)), "moe_route_grouped_dispatch");
 }
 
 MOE_API size_t moe_ffn_workspace_bytes(int B, int k, int H, int I) {

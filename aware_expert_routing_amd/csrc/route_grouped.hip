@@ -8,176 +8,414 @@
 //   w   = s of the kept experts (/ their sum) * scale
 //
 // Without a bias experts are ranked by their logit (both scores grow with
-// it).  Ties go to the lower index.  Selection values are compared in 64
-// bits: a batch of 16384 tokens with 256 experts holds pairs of values closer
-// than an fp32 rounding at the border of a choice, and such a pair would be
-// picked by the rounding of the exponential.
+// it).  Ties go to the lower index.  The decisions are those of 64-bit
+// arithmetic: a batch of 16384 tokens with 256 experts holds pairs of values
+// closer than an fp32 rounding at the border of a choice, and such a pair
+// would be picked by the rounding of the exponential.  They are taken in fp32
+// where that is certain: every value carries a bound on its error, and a token
+// with a comparison inside the bounds (about one in a hundred) is routed again
+// in 64 bits by its wavefront.
+//
+// One wavefront per token; lane l owns the kP consecutive experts from kP l,
+// so that of equal values the lowest lane, and in it the first, is the lower
+// index.  A selection is a lane-local maximum over order keys and a 6-step DPP
+// maximum.  Group values go through LDS once (group sizes are the caller's).
+#include "dispatch.h"
 #include "internal.h"
 
 namespace moe {
 namespace {
 
-constexpr int kWave = 64;
-constexpr int kWaves = 4;                        // tokens per workgroup, one per wavefront
-constexpr int kPer = kMaxGroupedExperts / kWave; // experts per lane: e = lane + 64 j
+constexpr double kNegInf64 = -__builtin_huge_val();
+constexpr float kNegInf = -__builtin_huge_valf();
 
-// Order-preserving 64-bit key of a selection value; 0 = masked.
+// Order-preserving keys of selection values; 0 = masked (NaN and -inf).
+__device__ __forceinline__ uint32_t key32(float c) {
+    if (!(c > kNegInf)) return 0u;
+    const uint32_t b = __float_as_uint(c == 0.0f ? 0.0f : c);
+    return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+}
+__device__ __forceinline__ float key_value(uint32_t o) {
+    return __uint_as_float((o & 0x80000000u) ? (o & 0x7fffffffu) : ~o);
+}
 __device__ __forceinline__ uint64_t key64(double c) {
-    if (!(c > -__builtin_huge_val())) return 0ull;   // NaN and -inf
+    if (!(c > kNegInf64)) return 0ull;
     const uint64_t b = __builtin_bit_cast(uint64_t, c == 0.0 ? 0.0 : c);
     return (b >> 63) ? ~b : (b | 0x8000000000000000ull);
 }
-__device__ __forceinline__ uint64_t wave_max(uint64_t v) {
-#pragma unroll
-    for (int d = 32; d >= 1; d >>= 1) {
-        const uint64_t o = __shfl_xor(v, d, kWave);
-        v = o > v ? o : v;
-    }
-    return v;
+
+// max(v, v moved by a DPP control); 0 where the move does not reach.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint32_t max_dpp(uint32_t v) {
+    return max(v, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(v), CTRL, ROWS, 0xF, true)));
+}
+// Maximum over the wavefront, as a scalar: quads, half rows, rows, then row
+// 0 into 1 and 2 into 3, and row 1 into 2 and 3; lane 63 holds it.
+__device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) {
+    v = max_dpp<0xB1, 0xF>(v);
+    v = max_dpp<0x4E, 0xF>(v);
+    v = max_dpp<0x141, 0xF>(v);
+    v = max_dpp<0x140, 0xF>(v);
+    v = max_dpp<0x142, 0xA>(v);
+    v = max_dpp<0x143, 0xC>(v);
+    return static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(v), kWave - 1));
+}
+template <int CTRL>
+__device__ __forceinline__ float move_dpp(float v) {
+    return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), CTRL, 0xF, 0xF, false));
+}
+__device__ __forceinline__ float lane_value(float v, int l) {
+    return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), l));
+}
+// Sum over the wavefront, the same in every lane.
+__device__ __forceinline__ float wave_sum(float v) {
+    v += move_dpp<0xB1>(v);
+    v += move_dpp<0x4E>(v);
+    v += move_dpp<0x141>(v);
+    v += move_dpp<0x140>(v);
+    return (lane_value(v, 0) + lane_value(v, 16)) + (lane_value(v, 32) + lane_value(v, 48));
 }
 __device__ __forceinline__ double wave_sum(double v) {
 #pragma unroll
     for (int d = 32; d >= 1; d >>= 1) v += __shfl_xor(v, d, kWave);
     return v;
 }
+__device__ __forceinline__ uint64_t wave_max_u64(uint64_t v) {
+    const uint32_t hi = wave_max_u32(static_cast<uint32_t>(v >> 32));
+    const uint32_t lo = wave_max_u32(static_cast<uint32_t>(v >> 32) == hi ? static_cast<uint32_t>(v) : 0u);
+    return (static_cast<uint64_t>(hi) << 32) | lo;
+}
 
-__device__ __forceinline__ float load_logit(const float* p) { return *p; }
-__device__ __forceinline__ float load_logit(const uint16_t* p) { return __uint_as_float(static_cast<uint32_t>(*p) << 16); }
+// exp(x + lo) within 2 units of fp32: x log2(e) in two pieces, the second
+// applied to the result's first order.  x is held to [-100, 88], where every
+// step is finite (a score that this touches is below 2^-100).
+__device__ __forceinline__ float exp_f32(float x, float lo) {
+    x = fminf(fmaxf(x, -100.0f), 88.0f);
+    const float y = x * 1.44269502f;                       // log2(e), fp32
+    const float r = __builtin_fmaf(x, 1.44269502f, -y) + __builtin_fmaf(x, 1.92596300e-8f, lo * 1.44269502f);
+    const float e = __builtin_amdgcn_exp2f(y);
+    return __builtin_fmaf(e, r * 0.693147182f, e);
+}
 
-template <typename LT>
-__global__ __launch_bounds__(kWaves * kWave) void route_grouped_kernel(GroupedArgs a, const LT* __restrict__ logits) {
-    __shared__ double val[kWaves][kMaxGroupedExperts];
-    const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
-    const int i = blockIdx.x * kWaves + wave;
-    if (i >= a.B) return;   // whole wavefronts; no workgroup barrier below
-    const int B_real = a.n_valid != nullptr ? min(max(*a.n_valid, 0), a.B) : a.B;
-    const size_t out = static_cast<size_t>(i) * a.k;
-    if (i >= B_real) {
-        if (lane < a.k) {
-            a.idx[out + lane] = -1;
-            a.w[out + lane] = 0.0f;
-        }
-        return;
-    }
-    double s[kPer], c[kPer];
-    bool live[kPer];
-    double m = -__builtin_huge_val();
+__device__ __forceinline__ float as_float(float v) { return v; }
+__device__ __forceinline__ float as_float(uint16_t v) { return __uint_as_float(static_cast<uint32_t>(v) << 16); }
+
+// The kP logits of the calling lane's experts; -inf past the last expert.
+template <typename LT, int kP>
+__device__ __forceinline__ void load_logits(const LT* row, int N, int e0, bool wide, float (&l)[kP]) {
+    struct alignas(sizeof(LT) * kP) Group { LT v[kP]; };
+    if (wide) {   // rows of whole groups at aligned addresses
+        if (e0 < N) {
+            const Group g = *reinterpret_cast<const Group*>(row + e0);
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-        const int e = lane + kWave * j;
-        float l = e < a.N ? load_logit(logits + static_cast<size_t>(i) * a.N + e) : -__builtin_huge_valf();
-        l = l > 3.402823466e38f ? 3.402823466e38f : l;   // +inf counts as the largest float
-        live[j] = l > -__builtin_huge_valf();
-        s[j] = live[j] ? static_cast<double>(l) : -__builtin_huge_val();
+            for (int j = 0; j < kP; ++j) l[j] = as_float(g.v[j]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < kP; ++j) l[j] = kNegInf;
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < kP; ++j) l[j] = e0 + j < N ? as_float(row[e0 + j]) : kNegInf;
+    }
+}
+
+// What a token's selection gives: lane r < k holds the r-th pick (-1: none)
+// and its score, and every lane the sum of the scores.
+struct Picks {
+    int e;
+    float s, sum;
+};
+
+// Group stage, shared by both precisions: `val` holds the experts' values in
+// LDS (-inf: masked).  Lanes split into n_group bands of 1 << shift lanes
+// (n_group rounded up to a power of two); every lane of band g returns group
+// g's value.
+template <typename F>
+__device__ __forceinline__ F group_value(const F* val, const GroupedArgs& a, int per, int shift, bool sum2, int lane) {
+    const F none = static_cast<F>(kNegInf64);
+    const int g = lane >> shift, width = 1 << shift;
+    F m1 = none, m2 = none;
+    if (g < a.n_group)
+        for (int e = g * per + (lane & (width - 1)); e < (g + 1) * per; e += width) {
+            const F v = val[e];
+            m2 = v > m1 ? m1 : (v > m2 ? v : m2);
+            m1 = v > m1 ? v : m1;
+        }
+    for (int d = 1; d < width; d <<= 1) {
+        const F o1 = __shfl_xor(m1, d, kWave), o2 = __shfl_xor(m2, d, kWave);
+        const F lo = o1 > m1 ? m1 : o1, hi2 = o2 > m2 ? o2 : m2;
+        m1 = o1 > m1 ? o1 : m1;
+        m2 = lo > hi2 ? lo : hi2;
+    }
+    return (sum2 && m2 > none) ? m1 + m2 : m1;
+}
+
+// A token in 64 bits.
+template <int kP>
+__device__ __forceinline__ Picks route_exact(const GroupedArgs& a, const float (&l_in)[kP], double* val, int per, int shift) {
+    const int lane = threadIdx.x & (kWave - 1), e0 = kP * lane;
+    const bool by_logit = a.bias == nullptr, sum2 = a.group_top2 && per > 1;
+    double s[kP], c[kP];
+    uint64_t key[kP];
+    double m = kNegInf64;
+#pragma unroll
+    for (int j = 0; j < kP; ++j) {
+        s[j] = static_cast<double>(l_in[j]);
+        c[j] = s[j];
         m = s[j] > m ? s[j] : m;
     }
-    const bool rank_by_logit = a.bias == nullptr;
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) c[j] = s[j];
     if (a.softmax) {
 #pragma unroll
         for (int d = 32; d >= 1; d >>= 1) m = fmax(m, __shfl_xor(m, d, kWave));
         double z = 0.0;
 #pragma unroll
-        for (int j = 0; j < kPer; ++j) {
-            s[j] = live[j] ? exp(s[j] - m) : 0.0;
+        for (int j = 0; j < kP; ++j) {
+            s[j] = c[j] > kNegInf64 ? exp(c[j] - m) : 0.0;
             z += s[j];
         }
         z = wave_sum(z);
 #pragma unroll
-        for (int j = 0; j < kPer; ++j) s[j] = z > 0.0 ? s[j] / z : 0.0;
+        for (int j = 0; j < kP; ++j) s[j] = z > 0.0 ? s[j] / z : 0.0;
     } else {
 #pragma unroll
-        for (int j = 0; j < kPer; ++j) s[j] = live[j] ? 1.0 / (1.0 + exp(-s[j])) : 0.0;
+        for (int j = 0; j < kP; ++j) s[j] = c[j] > kNegInf64 ? 1.0 / (1.0 + exp(-c[j])) : 0.0;
     }
-    const int per = a.N / a.n_group;
-    const bool sum2 = a.group_top2 && per > 1;
-    uint64_t key[kPer];
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-        const int e = lane + kWave * j;
-        if (!rank_by_logit && live[j]) c[j] = s[j] + static_cast<double>(a.bias[e]);
-        key[j] = live[j] ? key64(c[j]) : 0ull;
-        // the value that ranks groups: the score itself where two are added
-        const double g = (rank_by_logit && sum2) ? s[j] : c[j];
-        if (e < a.N) val[wave][e] = key[j] != 0ull ? g : -__builtin_huge_val();
+    for (int j = 0; j < kP; ++j) {
+        const int e = e0 + j;
+        if (!by_logit && c[j] > kNegInf64) c[j] = s[j] + static_cast<double>(a.bias[e]);
+        key[j] = key64(c[j]);
+        if (a.n_group > 1 && e < a.N) val[e] = key[j] != 0ull ? ((by_logit && sum2) ? s[j] : c[j]) : kNegInf64;
     }
     if (a.n_group > 1) {
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         __builtin_amdgcn_wave_barrier();
-        double g = -__builtin_huge_val();
-        if (lane < a.n_group) {
-            double m1 = -__builtin_huge_val(), m2 = m1;
-            for (int e = 0; e < per; ++e) {
-                const double v = val[wave][lane * per + e];
-                if (v > m1) {
-                    m2 = m1;
-                    m1 = v;
-                } else if (v > m2) {
-                    m2 = v;
-                }
-            }
-            g = (sum2 && m2 > -__builtin_huge_val()) ? m1 + m2 : m1;
+        const double g = group_value(val, a, per, shift, sum2, lane);
+        int rank = 0;
+        for (int o = 0; o < a.n_group; ++o) {
+            const double v = __shfl(g, o << shift, kWave);
+            rank += v > g || (v == g && o < (lane >> shift));
         }
-        uint64_t gk = lane < a.n_group ? key64(g) : 0ull;
-        uint64_t kept = 0ull;
-        for (int r = 0; r < a.topk_group; ++r) {
-            const uint64_t best = wave_max(gk);
-            if (best == 0ull) break;
-            const int o = __ffsll(static_cast<unsigned long long>(__ballot(gk == best))) - 1;
-            kept |= 1ull << o;
-            if (lane == o) gk = 0ull;
-        }
+        const uint64_t kept = __ballot(rank < a.topk_group);
 #pragma unroll
-        for (int j = 0; j < kPer; ++j)
-            if (!((kept >> (min(lane + kWave * j, a.N - 1) / per)) & 1ull)) key[j] = 0ull;
+        for (int j = 0; j < kP; ++j)
+            if (e0 + j >= a.N || !((kept >> ((e0 + j) / per << shift)) & 1ull)) key[j] = 0ull;
     }
-    // k selections; lane r keeps the r-th pick
-    int pick = -1;
+    Picks out{-1, 0.0f, 0.0f};
     double ps = 0.0;
     for (int r = 0; r < a.k; ++r) {
         uint64_t best = 0ull;
         int bj = 0;
+        double bs = 0.0;
 #pragma unroll
-        for (int j = 0; j < kPer; ++j)
+        for (int j = 0; j < kP; ++j)
             if (key[j] > best) {
                 best = key[j];
                 bj = j;
+                bs = s[j];
             }
-        const uint64_t top = wave_max(best);
+        const uint64_t top = wave_max_u64(best);
         if (top == 0ull) break;
-        // among the lanes that hold it, the lowest expert (e = lane + 64 j)
-        int e = best == top ? lane + kWave * bj : 0x7fffffff;
+        const int owner = __ffsll(static_cast<unsigned long long>(__ballot(best == top))) - 1;
+        const int e = kP * owner + __builtin_amdgcn_readlane(bj, owner);
+        const double se = __shfl(bs, owner, kWave);
 #pragma unroll
-        for (int d = 32; d >= 1; d >>= 1) e = min(e, __shfl_xor(e, d, kWave));
-        double se = 0.0;
-#pragma unroll
-        for (int j = 0; j < kPer; ++j)
-            if (e == lane + kWave * j) {
-                key[j] = 0ull;
-                se = s[j];
-            }
-        se = __shfl(se, e & (kWave - 1), kWave);
+        for (int j = 0; j < kP; ++j)
+            if (lane == owner && j == bj) key[j] = 0ull;
         if (lane == r) {
-            pick = e;
+            out.e = e;
             ps = se;
         }
     }
+    // (rounded to fp32 after the division, so that tiny scores keep their ratio)
     const double sum = wave_sum(ps);
-    if (a.renorm) ps = sum > 0.0 ? ps / sum : 0.0;
-    if (lane < a.k) {
-        a.idx[out + lane] = pick;
-        a.w[out + lane] = static_cast<float>(ps * static_cast<double>(a.scale));
+    out.s = static_cast<float>(a.renorm ? (sum > 0.0 ? ps / sum : 0.0) : ps);
+    out.sum = 1.0f;
+    return out;
+}
+
+// Bounds on the fp32 values' errors: a score is within kScoreErr of the row's
+// largest possible score, a sum within half a unit of its size more.
+constexpr float kSigmoidErr = 0x1p-21f, kSoftmaxErr = 0x1p-19f;
+
+// One token: the wavefront's lanes hold its logits (masked ones -inf).
+template <int kP>
+__device__ __forceinline__ Picks route_token(const GroupedArgs& a, const float (&l)[kP], double* lds, int per,
+                                             int shift, uint32_t per_magic) {
+    const int lane = threadIdx.x & (kWave - 1), e0 = kP * lane;
+    const bool by_logit = a.bias == nullptr, sum2 = a.group_top2 && per > 1;
+    float s[kP];
+    uint32_t key[kP];
+    float err;   // of a score
+    if (a.softmax) {
+        uint32_t km = 0u;
+#pragma unroll
+        for (int j = 0; j < kP; ++j) km = max(km, key32(l[j]));
+        const float m = key_value(wave_max_u32(km));   // (an empty row: NaN, and every expert masked)
+        float z = 0.0f;
+#pragma unroll
+        for (int j = 0; j < kP; ++j) {
+            const float d = l[j] - m, b = d - l[j];   // l - m = d + (l - (d - b)) - (m + b), exactly
+            s[j] = l[j] > kNegInf ? exp_f32(d, (l[j] - (d - b)) - (m + b)) : 0.0f;
+            z += s[j];
+        }
+        const float inv = 1.0f / wave_sum(z);
+#pragma unroll
+        for (int j = 0; j < kP; ++j) s[j] *= inv;
+        err = kSoftmaxErr * inv;
+    } else {
+#pragma unroll
+        for (int j = 0; j < kP; ++j) s[j] = l[j] > kNegInf ? __builtin_amdgcn_rcpf(1.0f + exp_f32(-l[j], 0.0f)) : 0.0f;
+        err = kSigmoidErr;
     }
+    bool unsure = false;
+    float* val = reinterpret_cast<float*>(lds);
+#pragma unroll
+    for (int j = 0; j < kP; ++j) {
+        const int e = e0 + j;
+        float c = l[j];
+        if (!by_logit && c > kNegInf) c = s[j] + a.bias[e];
+        key[j] = key32(c);
+        if (a.n_group > 1 && e < a.N) val[e] = key[j] != 0u ? ((by_logit && sum2) ? s[j] : c) : kNegInf;
+    }
+    if (a.n_group > 1) {
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        const float g = group_value(val, a, per, shift, sum2, lane);
+        const int mine = lane >> shift;
+        uint64_t kept;
+        if (by_logit && !sum2) {   // logits: exact
+            int rank = 0;
+            for (int o = 0; o < a.n_group; ++o) {
+                const float v = lane_value(g, o << shift);
+                rank += v > g || (v == g && o < mine);
+            }
+            kept = __ballot(rank < a.topk_group);
+        } else {
+            // groups surely and possibly above this one
+            int sure = 0, maybe = 0;
+            const float slack = 4.0f * err + 0x1p-22f * __builtin_fabsf(g);
+            for (int o = 0; o < a.n_group; ++o) {
+                const float v = lane_value(g, o << shift);
+                const float e = __builtin_fmaf(0x1p-22f, __builtin_fabsf(v), slack);
+                sure += v - g > e;
+                maybe += !(g - v > e) && o != mine;   // (also where an infinity leaves no difference)
+            }
+            const bool live = g > kNegInf;
+            const bool in = live && maybe < a.topk_group;
+            kept = __ballot(in);
+            unsure = __any(mine < a.n_group && live && !in && sure < a.topk_group);
+        }
+#pragma unroll
+        for (int j = 0; j < kP; ++j) {
+            const int group = static_cast<int>((static_cast<uint32_t>(e0 + j) * per_magic) >> 20);
+            if (e0 + j >= a.N || !((kept >> (group << shift)) & 1ull)) key[j] = 0u;
+        }
+    }
+    Picks out{-1, 0.0f, 0.0f};
+    if (!unsure) {
+        float last = 0.0f, least = 1.0f;
+        for (int r = 0; r <= a.k; ++r) {   // the last round only compares
+            uint32_t best = key[0];
+            int bj = 0;
+            float bs = s[0];
+#pragma unroll
+            for (int j = 1; j < kP; ++j) {
+                const bool up = key[j] > best;
+                best = up ? key[j] : best;
+                bj = up ? j : bj;
+                bs = up ? s[j] : bs;
+            }
+            const uint32_t top = wave_max_u32(best);
+            if (top == 0u) break;
+            const float v = key_value(top);
+            if (!by_logit && r > 0 &&
+                !(last - v > 2.0f * err + 0x1p-22f * (__builtin_fabsf(last) + __builtin_fabsf(v)))) {
+                unsure = true;
+                break;
+            }
+            last = v;
+            if (r == a.k) break;
+            const int owner = __ffsll(static_cast<unsigned long long>(__ballot(best == top))) - 1;
+            const int e = kP * owner + __builtin_amdgcn_readlane(bj, owner);
+            const float se = lane_value(bs, owner);
+            // two equal values: the lower index was taken; without a bias that is exact
+            const bool own = lane == owner;
+#pragma unroll
+            for (int j = 0; j < kP; ++j) key[j] = (own && j == bj) ? 0u : key[j];
+            out.e = lane == r ? e : out.e;
+            out.s = lane == r ? se : out.s;
+            out.sum += se;
+            least = fminf(least, se);
+        }
+        // scores near the end of fp32's range lose their ratio
+        unsure = unsure || least < 0x1p-100f;
+    }
+    if (__builtin_amdgcn_readfirstlane(static_cast<int>(unsure))) return route_exact<kP>(a, l, lds, per, shift);
+    if (a.renorm) out.s = out.sum > 0.0f ? out.s / out.sum : 0.0f;
+    return out;
+}
+
+// W tokens per workgroup, one per wavefront.  kDispatch: the workgroup that
+// finishes last dispatches the batch (it counts in a.sync).
+template <typename LT, int kP, int W, bool kDispatch>
+__global__ __launch_bounds__(W* kWave) void route_grouped_kernel(GroupedArgs a, int shift, uint32_t per_magic,
+                                                                 int wide) {
+    __shared__ double lds[W][kP * kWave];
+    const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
+    const int i = blockIdx.x * W + wave;
+    const int B_real = a.n_valid != nullptr ? min(max(*a.n_valid, 0), a.B) : a.B;
+    if (i < a.B) {   // whole wavefronts
+        Picks p{-1, 0.0f, 0.0f};
+        if (i < B_real) {
+            float l[kP];
+            load_logits<LT, kP>(static_cast<const LT*>(a.logits) + static_cast<size_t>(i) * a.N, a.N, kP * lane,
+                                wide != 0, l);
+#pragma unroll
+            for (int j = 0; j < kP; ++j) {   // NaN masks; +inf counts as the largest float
+                l[j] = l[j] > 3.402823466e38f ? 3.402823466e38f : l[j];
+                l[j] = l[j] > kNegInf ? l[j] : kNegInf;
+            }
+            p = route_token<kP>(a, l, lds[wave], a.N / a.n_group, shift, per_magic);
+        }
+        if (lane < a.k) {
+            a.idx[static_cast<size_t>(i) * a.k + lane] = p.e;
+            a.w[static_cast<size_t>(i) * a.k + lane] = p.s * a.scale;
+        }
+    }
+    if constexpr (kDispatch)
+        group_dispatch_last(a.idx, a.B, a.N, a.k, a.sync, true, a.cnt, a.offsets, a.perm, a.active, a.T, nullptr,
+                            nullptr);
+}
+
+template <typename LT, int kP>
+void launch(const GroupedArgs& a, hipStream_t s) {
+    const int per = a.N / a.n_group;
+    int shift = 6;   // lanes per group: 64 over n_group rounded up to a power of two
+    while ((1 << (6 - shift)) < a.n_group) --shift;
+    const uint32_t magic = ((1u << 20) + per - 1) / per;   // e / per = (e * magic) >> 20 for e < 512
+    const int wide = a.N % kP == 0 && reinterpret_cast<uintptr_t>(a.logits) % (sizeof(LT) * kP) == 0;
+    if (a.perm != nullptr) {
+        if constexpr (kP <= 2)
+            route_grouped_kernel<LT, kP, 16, true><<<(a.B + 15) / 16, 16 * kWave, 0, s>>>(a, shift, magic, wide);
+    } else {
+        route_grouped_kernel<LT, kP, 4, false><<<(a.B + 3) / 4, 4 * kWave, 0, s>>>(a, shift, magic, wide);
+    }
+}
+
+template <typename LT>
+void launch_for(const GroupedArgs& a, hipStream_t s) {
+    if (a.N <= 64) launch<LT, 1>(a, s);
+    else if (a.N <= 128) launch<LT, 2>(a, s);
+    else if (a.N <= 256) launch<LT, 4>(a, s);
+    else launch<LT, 8>(a, s);
 }
 
 }  // namespace
 
 hipError_t launch_route_grouped(const GroupedArgs& a, hipStream_t s) {
-    const unsigned grid = (a.B + kWaves - 1) / kWaves;
-    if (a.logits_dtype == MOE_DT_BF16)
-        route_grouped_kernel<uint16_t><<<grid, kWaves * kWave, 0, s>>>(a, static_cast<const uint16_t*>(a.logits));
-    else
-        route_grouped_kernel<float><<<grid, kWaves * kWave, 0, s>>>(a, static_cast<const float*>(a.logits));
+    if (a.logits_dtype == MOE_DT_BF16) launch_for<uint16_t>(a, s);
+    else launch_for<float>(a, s);
     return hipGetLastError();
 }
 
