@@ -312,32 +312,50 @@ def router_route_dispatch(x, w_r, k: int, mode: str, k0: int = 0, p: float = 1.0
     return logits, route, disp
 
 
-def _check_tensor(t, dtype, shape, device, name: str) -> None:
-    """A tensor the kernels index without further checks: wrong placement,
-    type, shape or layout is refused here."""
+def _check_tensor(t, dtype, shape, dev: int, name: str) -> None:
+    """A tensor the kernels index without further checks: wrong placement
+    (dev: the GPU's index), type, shape or layout is refused here."""
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+        return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a tensor, got {type(t).__name__}")
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}, is on {t.device}")
-    if t.dtype != dtype:
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on cuda:{dev}, is on {t.device}")
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, is {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, has {tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+    raise ValueError(f"{name} must be contiguous")
 
 
-def _check_device(t, name: str):
-    """The device of a call's main input: it has to be the current GPU, whose
-    current stream the call uses."""
+def _check_word(t, dev: int, name: str) -> None:
+    """An optional device int32 word (n_valid, sync)."""
+    if t is None or (isinstance(t, torch.Tensor) and t.dtype is torch.int32 and t.get_device() == dev and t.numel() > 0):
+        return
+    raise ValueError(f"{name} must be a non-empty int32 tensor on cuda:{dev}")
+
+
+def _check_device(t, name: str) -> int:
+    """The index of a call's main input's GPU: it has to be the current one,
+    whose current stream the call uses."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a tensor, got {type(t).__name__}")
-    dev = t.device
-    if dev.type != "cuda":
-        raise ValueError(f"{name} must be on the GPU, is on {dev}")
-    if dev.index != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {dev}, but the current device is cuda:{torch.cuda.current_device()}")
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError(f"{name} must be on the GPU, is on {t.device}")
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"{name} is on cuda:{dev}, but the current device is cuda:{torch.cuda.current_device()}")
     return dev
+
+
+def _stream_on(stream, dev: int) -> int:
+    """_stream for a call whose device is known to be the current one."""
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
+
+
+def _at(t) -> int | None:
+    """The address of a tensor that has been checked (None: none)."""
+    return None if t is None else t.data_ptr()
 
 
 def _scratch(stream, *shape, device, dtype, zero: bool = False):
@@ -352,22 +370,25 @@ def _scratch(stream, *shape, device, dtype, zero: bool = False):
         return new(*shape, device=device, dtype=dtype)
 
 
-def _grouped_args(logits, k, score, bias, n_group, topk_group, group_score, n_valid):
-    """Checks shared by the grouped-routing calls; returns (B, N, device, score, group score, topk_group)."""
+_SCORES = {"softmax": MOE_SCORE_SOFTMAX, "sigmoid": MOE_SCORE_SIGMOID}
+_GROUP_SCORES = {"max": MOE_GROUP_MAX, "top2": MOE_GROUP_TOP2}
+
+
+def _grouped_args(logits, score, bias, group_score, n_valid):
+    """Checks shared by the grouped-routing calls; returns (B, N, GPU index, score, group score)."""
     dev = _check_device(logits, "logits")
     if logits.dim() != 2:
         raise ValueError(f"logits must be [B, N], has shape {tuple(logits.shape)}")
     B, N = logits.shape
-    _check_tensor(logits, logits.dtype, (B, N), dev, "logits")
+    if not logits.is_contiguous():
+        raise ValueError("logits must be contiguous")
     if bias is not None:
         _check_tensor(bias, torch.float32, (N,), dev, "bias")
-    _check_i32_table(n_valid, 1, "n_valid", dev)
-    try:
-        sc = {"softmax": MOE_SCORE_SOFTMAX, "sigmoid": MOE_SCORE_SIGMOID}[score]
-        gs = {"max": MOE_GROUP_MAX, "top2": MOE_GROUP_TOP2}[group_score]
-    except KeyError as e:
-        raise ValueError(f"unknown score or group_score {e}") from None
-    return B, N, dev, sc, gs, n_group if topk_group is None else int(topk_group)
+    _check_word(n_valid, dev, "n_valid")
+    sc, gs = _SCORES.get(score), _GROUP_SCORES.get(group_score)
+    if sc is None or gs is None:
+        raise ValueError(f"unknown score {score!r} or group_score {group_score!r}")
+    return B, N, dev, sc, gs
 
 
 def route_grouped(logits, k: int, score: str = "sigmoid", bias=None, n_group: int = 1,
@@ -375,16 +396,21 @@ def route_grouped(logits, k: int, score: str = "sigmoid", bias=None, n_group: in
                   scale: float = 1.0, n_valid=None, idx=None, w=None, stream=None):
     """Grouped routing (moe_route_grouped): scores "softmax" or "sigmoid", an
     fp32 bias [N] that moves the choice but not the weights, the topk_group
-    best of n_group groups ranked by "max" or "top2", the k best experts in
-    them.  logits [B, N] fp32 or bf16.  Returns (idx, w), both [B, k]."""
-    B, N, dev, sc, gs, tg = _grouped_args(logits, k, score, bias, n_group, topk_group, group_score, n_valid)
-    idx = _scratch(stream, B, k, device=dev, dtype=torch.int32) if idx is None else idx
-    w = _scratch(stream, B, k, device=dev, dtype=torch.float32) if w is None else w
-    _check_tensor(idx, torch.int32, (B, k), dev, "idx")
-    _check_tensor(w, torch.float32, (B, k), dev, "w")
+    best of n_group groups (None: all) ranked by "max" or "top2", the k best
+    experts in them.  logits [B, N] fp32 or bf16.  Returns (idx, w), both [B, k]."""
+    B, N, dev, sc, gs = _grouped_args(logits, score, bias, group_score, n_valid)
+    if idx is None:
+        idx = _scratch(stream, B, k, device=logits.device, dtype=torch.int32)
+    else:
+        _check_tensor(idx, torch.int32, (B, k), dev, "idx")
+    if w is None:
+        w = _scratch(stream, B, k, device=logits.device, dtype=torch.float32)
+    else:
+        _check_tensor(w, torch.float32, (B, k), dev, "w")
     _check("moe_route_grouped", lib().moe_route_grouped(
-        _ptr(logits), _x_dtype(logits), _ptr(bias), B, N, k, sc, n_group, tg, gs, int(bool(renorm)), float(scale),
-        _ptr(n_valid), _ptr(idx), _ptr(w), _stream(stream)))
+        logits.data_ptr(), _x_dtype(logits), _at(bias), B, N, k, sc, n_group,
+        n_group if topk_group is None else topk_group, gs, bool(renorm), scale, _at(n_valid), idx.data_ptr(),
+        w.data_ptr(), _stream_on(stream, dev)))
     return idx, w
 
 
@@ -394,23 +420,31 @@ def route_grouped_dispatch(logits, k: int, score: str = "sigmoid", bias=None, n_
     """Grouped routing followed by dispatch (moe_route_grouped_dispatch).
     sync: device int32 [1] that starts at zero (allocated here if None).
     Returns (route, disp) dicts as route_dispatch does."""
-    B, N, dev, sc, gs, tg = _grouped_args(logits, k, score, bias, n_group, topk_group, group_score, n_valid)
-    i32 = dict(device=dev, dtype=torch.int32)
+    B, N, dev, sc, gs = _grouped_args(logits, score, bias, group_score, n_valid)
+    i32 = dict(device=logits.device, dtype=torch.int32)
     if route is None:
-        route = dict(idx=_scratch(stream, B, k, **i32), w=_scratch(stream, B, k, device=dev, dtype=torch.float32))
+        route = dict(idx=_scratch(stream, B, k, **i32),
+                     w=_scratch(stream, B, k, device=logits.device, dtype=torch.float32))
     if disp is None:
         disp = {name: _scratch(stream, n, **i32)
                 for name, n in (("cnt", N), ("offsets", N + 1), ("perm", B * k), ("active", N), ("T", 1))}
-    sync = _scratch(stream, 1, **i32, zero=True) if sync is None else sync
-    _check_tensor(route["idx"], torch.int32, (B, k), dev, "idx")
-    _check_tensor(route["w"], torch.float32, (B, k), dev, "w")
-    for name, n in (("cnt", N), ("offsets", N + 1), ("perm", B * k), ("active", N), ("T", 1)):
-        _check_tensor(disp[name], torch.int32, (n,), dev, name)
-    _check_i32_table(sync, 1, "sync", dev)
+    if sync is None:
+        sync = _scratch(stream, 1, **i32, zero=True)
+    idx, w, cnt, offsets, perm = route["idx"], route["w"], disp["cnt"], disp["offsets"], disp["perm"]
+    active, T, i = disp["active"], disp["T"], torch.int32
+    _check_tensor(idx, i, (B, k), dev, "idx")
+    _check_tensor(w, torch.float32, (B, k), dev, "w")
+    _check_tensor(cnt, i, (N,), dev, "cnt")
+    _check_tensor(offsets, i, (N + 1,), dev, "offsets")
+    _check_tensor(perm, i, (B * k,), dev, "perm")
+    _check_tensor(active, i, (N,), dev, "active")
+    _check_tensor(T, i, (1,), dev, "T")
+    _check_word(sync, dev, "sync")
     _check("moe_route_grouped_dispatch", lib().moe_route_grouped_dispatch(
-        _ptr(logits), _x_dtype(logits), _ptr(bias), B, N, k, sc, n_group, tg, gs, int(bool(renorm)), float(scale),
-        _ptr(n_valid), _ptr(route["idx"]), _ptr(route["w"]), _ptr(disp["cnt"]), _ptr(disp["offsets"]),
-        _ptr(disp["perm"]), _ptr(disp["active"]), _ptr(disp["T"]), _ptr(sync), _stream(stream)))
+        logits.data_ptr(), _x_dtype(logits), _at(bias), B, N, k, sc, n_group,
+        n_group if topk_group is None else topk_group, gs, bool(renorm), scale, _at(n_valid), idx.data_ptr(),
+        w.data_ptr(), cnt.data_ptr(), offsets.data_ptr(), perm.data_ptr(), active.data_ptr(), T.data_ptr(),
+        sync.data_ptr(), _stream_on(stream, dev)))
     return route, disp
 
 
@@ -455,10 +489,10 @@ def lora_pack(a, b, stream=None):
     _check_tensor(a, torch.bfloat16, (rank, H), dev, "A")
     _check_tensor(b, torch.bfloat16, (O, rank), dev, "B")
     R = (rank + 15) // 16 * 16
-    dst_a = _scratch(stream, R, H, device=dev, dtype=torch.bfloat16)
-    dst_b = _scratch(stream, O, R, device=dev, dtype=torch.bfloat16)
+    dst_a = _scratch(stream, R, H, device=a.device, dtype=torch.bfloat16)
+    dst_b = _scratch(stream, O, R, device=a.device, dtype=torch.bfloat16)
     _check("moe_lora_pack", lib().moe_lora_pack(_ptr(a), _ptr(b), rank, H, O, _ptr(dst_a), _ptr(dst_b),
-                                                _stream(stream)))
+                                                _stream_on(stream, dev)))
     return dst_a, dst_b, R
 
 
@@ -468,13 +502,13 @@ def lora_publish(table, i: int, h: LoraHandle, stream=None):
     _check_tensor(table, torch.uint8, (table.numel(),), dev, "table")
     if not 0 <= i < table.numel() // LORA_HANDLE_BYTES:
         raise ValueError(f"adapter {i} is outside the table")
-    _check("moe_lora_publish", lib().moe_lora_publish(_ptr(table), i, ctypes.byref(h), _stream(stream)))
+    _check("moe_lora_publish", lib().moe_lora_publish(_ptr(table), i, ctypes.byref(h), _stream_on(stream, dev)))
 
 
 def _dt(dtype) -> int:
-    if dtype == torch.bfloat16:
+    if dtype is torch.bfloat16:
         return MOE_DT_BF16
-    if dtype == torch.float32:
+    if dtype is torch.float32:
         return MOE_DT_F32
     raise TypeError(f"must be float32 or bfloat16, got {dtype}")
 
@@ -487,41 +521,50 @@ def shared_ffn_workspace_bytes(B: int, H: int, I: int, max_rank: int, x_dtype, y
     return int(lib().moe_shared_ffn_workspace_bytes(B, H, I, max_rank, _dt(x_dtype), _dt(y_dtype)))
 
 
-def _proj_args(x, y, y_dtype, O, adapter, tables, n_valid, ws, ws_bytes, accumulate, stream):
-    """Checks shared by lora_linear and shared_ffn.  tables: (LoraTable or
-    None, H, O) for each projection.  Returns (B, H, y, ws, n_adapters, max_rank)."""
+def _proj_args(x, H: int, O: int, y, y_dtype, accumulate, n_valid, stream):
+    """Checks of lora_linear's and shared_ffn's activations; returns (B, x's
+    type, y, y's type, GPU index)."""
     dev = _check_device(x, "x")
-    if x.dim() != 2:
-        raise ValueError(f"x must be [B, H], has shape {tuple(x.shape)}")
-    B, H = x.shape
-    _x_dtype(x)
-    _check_tensor(x, x.dtype, (B, H), dev, "x")
+    if x.dim() != 2 or x.shape[1] != H:
+        raise ValueError(f"x must be [B, {H}], has shape {tuple(x.shape)}")
+    if not x.is_contiguous():
+        raise ValueError("x must be contiguous")
+    B, xd = x.shape[0], _dt(x.dtype)
     if y is None:
         if accumulate:
             raise ValueError("accumulating needs the y to add to")
-        y = _scratch(stream, B, O, device=dev, dtype=x.dtype if y_dtype is None else y_dtype)
-    _dt(y.dtype)
-    _check_tensor(y, y.dtype if y_dtype is None else y_dtype, (B, O), dev, "y")
-    _check_i32_table(n_valid, 1, "n_valid", dev)
-    used = [(t, h, o) for t, h, o in tables if t is not None]
-    n = rank = 0
-    if used:
-        n, rank = used[0][0].n, max(t.max_rank for t, _, _ in used)
-        for t, h, o in used:
-            if (t.H, t.O) != (h, o):
-                raise ValueError(f"an adapter table of a [{t.O}, {t.H}] projection beside one of [{o}, {h}]")
-            if t.n != n:
-                raise ValueError("the adapter tables of one call must have the same number of entries")
-            _check_tensor(t.handles, torch.uint8, (n * LORA_HANDLE_BYTES,), dev, "adapter table")
+        y = _scratch(stream, B, O, device=x.device, dtype=x.dtype if y_dtype is None else y_dtype)
+    elif not isinstance(y, torch.Tensor):
+        raise TypeError(f"y must be a tensor, got {type(y).__name__}")
+    else:
+        _check_tensor(y, y.dtype if y_dtype is None else y_dtype, (B, O), dev, "y")
+    _check_word(n_valid, dev, "n_valid")
+    return B, xd, y, _dt(y.dtype), dev
+
+
+def _check_adapters(table, H: int, O: int, n: int, adapter, B: int, dev: int) -> int:
+    """One projection's adapter table, of n entries (0: the first of the call's
+    tables).  Returns its number of entries."""
+    if table.H != H or table.O != O:
+        raise ValueError(f"an adapter table of a [{table.O}, {table.H}] projection beside one of [{O}, {H}]")
+    if n and table.n != n:
+        raise ValueError("the adapter tables of one call must have the same number of entries")
+    _check_tensor(table.handles, torch.uint8, (table.n * LORA_HANDLE_BYTES,), dev, "adapter table")
+    if not n:
         if adapter is None:
             raise ValueError("adapter tables need the tokens' adapter ids")
         _check_tensor(adapter, torch.int32, (B,), dev, "adapter")
-    need = ws_bytes(B, H, rank, x.dtype, y.dtype)
-    if ws is None and need:
-        ws = _scratch(stream, need, device=dev, dtype=torch.uint8)
-    if ws is not None and (ws.device != dev or not ws.is_contiguous()):
-        raise ValueError(f"ws must be contiguous on {dev}")
-    return B, H, y, ws, n, rank
+    return table.n
+
+
+def _workspace(ws, need, stream, x):
+    """A caller's workspace (its size and alignment are the library's check), or one of need() bytes."""
+    if ws is None:
+        n = need()
+        return _scratch(stream, n, device=x.device, dtype=torch.uint8) if n else None
+    if not isinstance(ws, torch.Tensor) or ws.get_device() != x.get_device() or not ws.is_contiguous():
+        raise ValueError(f"ws must be a contiguous tensor on {x.device}")
+    return ws
 
 
 def lora_linear(x, w, lora=None, adapter=None, y=None, y_dtype=None, accumulate: bool = False, n_valid=None, ws=None,
@@ -534,14 +577,19 @@ def lora_linear(x, w, lora=None, adapter=None, y=None, y_dtype=None, accumulate:
     y_dtype, if None); accumulate adds to an fp32 y; rows at or past n_valid
     (device int32 [1]) are left as they are.
     """
-    O = w.shape[0]
-    B, H, y, ws, n, rank = _proj_args(x, y, y_dtype, O, adapter, [(lora, x.shape[-1], O)], n_valid, ws,
-                                      lambda B, H, r, xd, yd: lora_workspace_bytes(B, H, O, r, xd, yd), accumulate, stream)
-    _check_tensor(w, torch.bfloat16, (O, H), x.device, "w")
+    if not isinstance(w, torch.Tensor) or w.dim() != 2:
+        raise TypeError("w must be a packed [O, H] tensor")
+    O, H = w.shape
+    B, xd, y, yd, dev = _proj_args(x, H, O, y, y_dtype, accumulate, n_valid, stream)
+    _check_tensor(w, torch.bfloat16, (O, H), dev, "w")
+    table, n, rank, ids = None, 0, 0, None
+    if lora is not None:
+        n = _check_adapters(lora, H, O, 0, adapter, B, dev)
+        table, rank, ids = lora.handles.data_ptr(), lora.max_rank, adapter.data_ptr()
+    ws = _workspace(ws, lambda: lora_workspace_bytes(B, H, O, rank, x.dtype, y.dtype), stream, x)
     _check("moe_lora_linear", lib().moe_lora_linear(
-        _ptr(w), None if lora is None else _ptr(lora.handles), n, rank, None if lora is None else _ptr(adapter),
-        _ptr(x), _x_dtype(x), B, H, O, _ptr(n_valid), _ptr(y), _dt(y.dtype), int(bool(accumulate)), _ptr(ws),
-        0 if ws is None else ws.numel() * ws.element_size(), _stream(stream)))
+        w.data_ptr(), table, n, rank, ids, x.data_ptr(), xd, B, H, O, _at(n_valid), y.data_ptr(), yd, bool(accumulate),
+        _at(ws), 0 if ws is None else ws.numel() * ws.element_size(), _stream_on(stream, dev)))
     return y
 
 
@@ -552,23 +600,30 @@ def shared_ffn(x, shared, loras=None, adapter=None, y=None, y_dtype=None, accumu
     Otherwise as lora_linear."""
     if shared.fmt != MOE_W_BF16:
         raise ValueError("the shared expert's weights must be bf16")
-    I, H = shared.gate.shape
-    loras = (None, None, None) if loras is None else tuple(loras)
-    if len(loras) != 3:
-        raise ValueError("loras must be three tables (gate, up, down)")
-    B, Hx, y, ws, n, rank = _proj_args(x, y, y_dtype, H, adapter,
-                                       [(loras[0], H, I), (loras[1], H, I), (loras[2], I, H)], n_valid, ws,
-                                       lambda B, H, r, xd, yd: shared_ffn_workspace_bytes(B, H, I, r, xd, yd),
-                                       accumulate, stream)
-    if Hx != H:
-        raise ValueError(f"x has {Hx} columns, the shared expert {H}")
-    for name, t, shape in (("gate", shared.gate, (I, H)), ("up", shared.up, (I, H)), ("down", shared.down, (H, I))):
-        _check_tensor(t, torch.bfloat16, shape, x.device, name)
-    h = shared.handle()
+    gate, up, down = shared.gate, shared.up, shared.down
+    I, H = gate.shape
+    B, xd, y, yd, dev = _proj_args(x, H, H, y, y_dtype, accumulate, n_valid, stream)
+    bf = torch.bfloat16
+    _check_tensor(gate, bf, (I, H), dev, "gate")
+    _check_tensor(up, bf, (I, H), dev, "up")
+    _check_tensor(down, bf, (H, I), dev, "down")
+    tg = tu = td = ids = None
+    n = rank = 0
+    if loras is not None:
+        lg, lu, ld = loras
+        if lg is not None:
+            n, tg, rank = _check_adapters(lg, H, I, n, adapter, B, dev), lg.handles.data_ptr(), lg.max_rank
+        if lu is not None:
+            n, tu, rank = _check_adapters(lu, H, I, n, adapter, B, dev), lu.handles.data_ptr(), max(rank, lu.max_rank)
+        if ld is not None:
+            n, td, rank = _check_adapters(ld, I, H, n, adapter, B, dev), ld.handles.data_ptr(), max(rank, ld.max_rank)
+        if n:
+            ids = adapter.data_ptr()
+    ws = _workspace(ws, lambda: shared_ffn_workspace_bytes(B, H, I, rank, x.dtype, y.dtype), stream, x)
+    h = ExpertHandle(MOE_W_BF16, 0, gate.data_ptr(), up.data_ptr(), down.data_ptr())
     _check("moe_shared_ffn", lib().moe_shared_ffn(
-        ctypes.byref(h), *[None if t is None else _ptr(t.handles) for t in loras], n, rank,
-        None if rank == 0 else _ptr(adapter), _ptr(x), _x_dtype(x), B, H, I, _ptr(n_valid), _ptr(y), _dt(y.dtype),
-        int(bool(accumulate)), _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(), _stream(stream)))
+        h, tg, tu, td, n, rank, ids, x.data_ptr(), xd, B, H, I, _at(n_valid), y.data_ptr(), yd, bool(accumulate),
+        _at(ws), 0 if ws is None else ws.numel() * ws.element_size(), _stream_on(stream, dev)))
     return y
 
 

@@ -762,29 +762,68 @@ __global__ __launch_bounds__(kFinishWaves* kWave) void proj_finish_kernel(ProjAr
 // Tiled projection, for many tokens: a workgroup of WR x WC waves owns
 // 16 WR MB rows of W (for NM = 2 half of them gate rows and half the up rows of
 // the same outputs) and 16 WC NB tokens; a wave owns MB x NB blocks of 16 x 16
-// in accumulators.  Two column tiles at a time are copied to LDS in operand
-// order (a packed weight tile as it lies; of x the lane's 16 bytes of its
-// token's row), straight from memory (global_load_lds), into the half of a
-// double buffer that the products are not reading.
+// in accumulators.  Column tiles go to LDS in operand order (a packed weight
+// tile as it lies; of x the lane's 16 bytes of its token's row), straight from
+// memory (global_load_lds), kStages of them in a ring.
+//   Step s: wait until this wave's copies of step s + 1 have landed (those of
+//   step s + 2 stay in flight); barrier; start the copies of step s + 3 into the
+//   place of step s - 1, whose operands every wave has used by then; read the
+//   operands of step s + 1 while the products of step s run: x into a second
+//   set of registers, each row of W into the registers its last product has
+//   just left.  (The scheduling barriers keep that order: left to itself the
+//   compiler gathers the reads and waits for each.)
+// Steps past the last copy the last one again, so that the waits count alike;
+// nothing reads those.
 // ---------------------------------------------------------------------------
-typedef __attribute__((address_space(1))) const void* gptr;
 typedef __attribute__((address_space(3))) void* lptr;
+
+__device__ __forceinline__ const char* uniform(const char* p) {   // wave-uniform pointer into scalar registers
+    const uint64_t v = reinterpret_cast<uint64_t>(p);
+    const uint32_t lo = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(v));
+    const uint32_t hi = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(v >> 32));
+    return reinterpret_cast<const char*>((static_cast<uint64_t>(hi) << 32) | lo);
+}
+
+// 16 bytes per lane from base + lane_offset + offset (base and offset uniform)
+// to 1 KB at `to` in LDS.  A buffer load: the compiler waits for LDS reads all
+// together where a global load to LDS is in flight, and one by one here.
+__device__ __forceinline__ void copy_tile(const char* base, int lane_offset, int offset, char* to) {
+#ifdef __HIP_DEVICE_COMPILE__   // (the resource type does not exist in the host pass)
+    const __amdgpu_buffer_rsrc_t r =
+        __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(base), 0, 0x7fffffff, 0x00027000);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lptr)to, 16, lane_offset, offset, 0, 0);
+#endif
+}
+
+constexpr int kStages = 4;
+
+// At most N vector-memory operations of this wave still in flight; then the
+// workgroup's barrier.
+template <int N>
+__device__ __forceinline__ void wait_and_barrier() {
+    asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(N) : "memory");
+}
 
 template <int XK, int YK, int NM, int WR, int WC, int MB, int NB>
 __global__ __launch_bounds__(WR* WC* kWave) void proj_tile_kernel(ProjArgs a, int row_tiles, int tok_tiles) {
     constexpr int NW = WR * WC;
-    constexpr int RT = WR * MB, CT = WC * NB;      // 1 KB tiles per 32 columns
+    constexpr int RT = WR * MB, CT = WC * NB;      // 1 KB tiles per step of 32 columns
     constexpr int kStep = RT + CT;
-    constexpr int kStage = 2 * kStep * 1024;
-    constexpr int kPer = 2 * kStep / NW;           // tiles a wave copies per stage
-    static_assert(2 * kStep % NW == 0 && MB % NM == 0, "tile split");
+    constexpr int kPer = kStep / NW;               // tiles a wave copies per step
+    static_assert(kStep % NW == 0 && MB % NM == 0 && NB % 4 == 0, "tile split");
     constexpr int P = XK == kActPlanes ? 3 : 1;
-    __shared__ __align__(1024) char lds[2 * kStage];
-    const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
+    __shared__ __align__(1024) char lds[kStages * kStep * 1024];
+    const int lane = threadIdx.x & (kWave - 1);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int n = lane & 15, q = lane >> 4;
     const int wr = wave / WC, wc = wave % WC;
     const int B_real = real_tokens(a);
-    const int tile_r = blockIdx.x % row_tiles, tile_c = blockIdx.x / row_tiles;
+    // Workgroup id mod 8 is the XCD: each XCD gets a contiguous run of tiles,
+    // in bands of four row tiles, so that its L2 holds what they share.
+    const int all = row_tiles * tok_tiles, xcd = blockIdx.x & 7;
+    const int at = xcd * (all >> 3) + min(xcd, all & 7) + (static_cast<int>(blockIdx.x) >> 3);
+    const int band = at / (4 * tok_tiles), in = at - band * 4 * tok_tiles, wide = min(4, row_tiles - 4 * band);
+    const int tile_r = 4 * band + in % wide, tile_c = in / wide;
     const int i0 = tile_c * 16 * CT;
     if (i0 >= B_real) return;
     const int blocks = a.O / 16, S = a.H / 32, steps = P * S;
@@ -794,73 +833,95 @@ __global__ __launch_bounds__(WR* WC* kWave) void proj_tile_kernel(ProjArgs a, in
     auto mat_of = [](int j) { return NM == 1 ? 0 : (j % MB) / kHalf; };
     auto ob_of = [&](int j) { return min(ob0 + (NM == 1 ? j : (j / MB) * kHalf + j % kHalf), blocks - 1); };
 
-    const char* src[kPer];
+    // a tile's base (the same for the wavefront), the lane's offset from it, and the offset of a step
+    const char* base[kPer];
+    int offset[kPer];
 #pragma unroll
     for (int u = 0; u < kPer; ++u) {
-        const int slot = wave * kPer + u, j = slot >> 1;
-        if (j < RT)
-            src[u] = static_cast<const char*>(mat_of(j) ? a.w[1] : a.w[0]) + static_cast<size_t>(ob_of(j)) * S * 1024 +
-                     lane * 16;
-        else
-            src[u] = x_row<kActBf16>(a, min(i0 + 16 * (j - RT) + n, B_real - 1), q);
+        const int j = wave * kPer + u;
+        if (j < RT) {
+            base[u] = static_cast<const char*>(mat_of(j) ? a.w[1] : a.w[0]) + static_cast<size_t>(ob_of(j)) * S * 1024;
+            offset[u] = lane * 16;
+        } else {
+            const int i = i0 + 16 * (j - RT);   // (at most 256 rows of 32 KB behind i0)
+            base[u] = static_cast<const char*>(a.x) + static_cast<size_t>(i0) * a.H * 2;
+            offset[u] = (min(i + n, B_real - 1) - i0) * a.H * 2 + 16 * q;
+        }
+        base[u] = uniform(base[u]);
     }
-    auto copy = [&](int it, int buf) {
+    auto copy = [&](int step) {
+        const int kk = min(step, steps - 1);
+        const int plane = P == 1 ? 0 : P - 1 - kk / S;   // the smallest term first
+        const int s = P == 1 ? kk : kk % S;
+        char* to = lds + (step % kStages) * kStep * 1024;
 #pragma unroll
         for (int u = 0; u < kPer; ++u) {
-            const int slot = wave * kPer + u, j = slot >> 1;
-            const int kk = min(2 * it + (slot & 1), steps - 1);
-            const int plane = P == 1 ? 0 : P - 1 - kk / S;   // the smallest term first
-            const int s = P == 1 ? kk : kk % S;
-            const char* g = src[u] + (j < RT ? static_cast<size_t>(s) * 1024
-                                             : static_cast<size_t>(s) * 64 + static_cast<size_t>(plane) * a.x_plane);
-            __builtin_amdgcn_global_load_lds((gptr)g, (lptr)(lds + buf * kStage + ((slot & 1) * kStep + j) * 1024), 16,
-                                             0, 0);
+            const int j = wave * kPer + u;
+            const char* from = P == 1 || j < RT ? base[u] : base[u] + static_cast<size_t>(plane) * a.x_plane;
+            copy_tile(from, offset[u], s * (j < RT ? 1024 : 64), to + j * 1024);
         }
     };
 
-    f32x4 acc[MB][NB];
+    constexpr int Q = NB / 4;   // runs of 64 tokens
+    f32x4 acc[Q][MB][4];
 #pragma unroll
-    for (int j = 0; j < MB; ++j)
-#pragma unroll
-        for (int t = 0; t < NB; ++t) acc[j][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    copy(0, 0);
-    __syncthreads();
-    auto multiply = [&](int buf, int ks) {
-        const char* base = lds + buf * kStage + ks * kStep * 1024 + lane * 16;
-        u32x4 w[MB], x[NB];
-#pragma unroll
-        for (int t = 0; t < NB; ++t) x[t] = *reinterpret_cast<const u32x4*>(base + (RT + wc * NB + t) * 1024);
-#pragma unroll
-        for (int j = 0; j < MB; ++j) w[j] = *reinterpret_cast<const u32x4*>(base + (wr * MB + j) * 1024);
+    for (int h = 0; h < Q; ++h)
 #pragma unroll
         for (int j = 0; j < MB; ++j)
 #pragma unroll
-            for (int t = 0; t < NB; ++t) acc[j][t] = mma32(w[j], x[t], acc[j][t]);
+            for (int t = 0; t < 4; ++t) acc[h][j][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int s = 0; s < kStages - 1; ++s) copy(s);
+    wait_and_barrier<kPer*(kStages - 2)>();
+    const char* mine_w = lds + wr * MB * 1024 + lane * 16;
+    const char* mine_x = lds + (RT + wc * NB) * 1024 + lane * 16;
+    u32x4 w[MB], x0[NB], x1[NB];
+#pragma unroll
+    for (int t = 0; t < NB; ++t) x0[t] = *reinterpret_cast<const u32x4*>(mine_x + t * 1024);
+#pragma unroll
+    for (int j = 0; j < MB; ++j) w[j] = *reinterpret_cast<const u32x4*>(mine_w + j * 1024);
+    auto step = [&](int s, const u32x4 (&x)[NB], u32x4 (&xn)[NB]) {
+        wait_and_barrier<kPer*(kStages - 3)>();
+        copy(s + kStages - 1);
+        __builtin_amdgcn_sched_barrier(0);
+        const int next = ((s + 1) % kStages) * kStep * 1024;
+#pragma unroll
+        for (int j = 0; j < MB; ++j) {
+#pragma unroll
+            for (int t = j * NB / MB; t < (j + 1) * NB / MB; ++t)
+                xn[t] = *reinterpret_cast<const u32x4*>(mine_x + next + t * 1024);
+#pragma unroll
+            for (int t = 0; t < NB; ++t) acc[t / 4][j][t % 4] = mma32(w[j], x[t], acc[t / 4][j][t % 4]);
+            w[j] = *reinterpret_cast<const u32x4*>(mine_w + next + j * 1024);
+            __builtin_amdgcn_sched_barrier(0);
+        }
     };
-    const int its = (steps + 1) / 2;
-    for (int it = 0; it + 1 < its; ++it) {
-        copy(it + 1, (it & 1) ^ 1);
-        multiply(it & 1, 0);
-        multiply(it & 1, 1);
-        __syncthreads();
+    int s = 0;
+    for (; s + 1 < steps; s += 2) {
+        step(s, x0, x1);
+        step(s + 1, x1, x0);
     }
-    multiply((its - 1) & 1, 0);
-    if ((steps & 1) == 0) multiply((its - 1) & 1, 1);
-    expand<v_terms_for<YK>()>(a, i0 + 16 * NB * wc, B_real, acc,
-                              [&](int j) { return ob_of(wr * MB + j); }, [&](int j) { return mat_of(j); });
+    if (s < steps) step(s, x0, x1);
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // no copy may land after the workgroup's end
 #pragma unroll
-    for (int j = 0; j < kHalf; ++j) {
-        const int ob = ob0 + wr * kHalf + j;
-        if (ob >= blocks) continue;
+    for (int h = 0; h < Q; ++h) {
+        const int i1 = i0 + 16 * NB * wc + 64 * h;
+        expand<v_terms_for<YK>()>(a, i1, B_real, acc[h], [&](int j) { return ob_of(wr * MB + j); },
+                                  [&](int j) { return mat_of(j); });
 #pragma unroll
-        for (int t = 0; t < NB; ++t) {
-            const int i = i0 + 16 * (NB * wc + t) + n;
-            f32x4 r = acc[j][t];
-            if constexpr (NM == 2) {
+        for (int j = 0; j < kHalf; ++j) {
+            const int ob = ob0 + wr * kHalf + j;
+            if (ob >= blocks) continue;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) r[e] = silu(r[e]) * acc[j + kHalf][t][e];
+            for (int t = 0; t < 4; ++t) {
+                const int i = i1 + 16 * t + n;
+                f32x4 r = acc[h][j][t];
+                if constexpr (NM == 2) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) r[e] = silu(r[e]) * acc[h][j + kHalf][t][e];
+                }
+                if (i < B_real) store4<YK>(a, i, 16 * ob + 4 * q, r);
             }
-            if (i < B_real) store4<YK>(a, i, 16 * ob + 4 * q, r);
         }
     }
 }
@@ -1060,8 +1121,8 @@ size_t x_planes_bytes(int B, int H, int x_dtype) {   // fp32 x of more than kRow
 }
 // Partial blocks and item lists of a projection: the most any number of
 // adapters asks for.
-size_t part_bytes(int B, int H, int O, int mats) {
-    const Plan p = plan_proj(B, H, O, mats, kFusedBlocks + 1);
+size_t part_bytes(int B, int H, int O, int mats, int max_rank) {
+    const Plan p = plan_proj(B, H, O, mats, max_rank > 0 ? kFusedBlocks + 1 : 0);
     return up256(p.part_bytes + p.item_bytes + p.count_bytes);
 }
 
@@ -1082,7 +1143,7 @@ hipError_t cut_x(ProjArgs& a, void* ws, hipStream_t s) {
 
 // v, the planes of x, partial blocks.
 size_t lora_workspace_bytes(int B, int H, int O, int max_rank, int x_dtype) {
-    return v_bytes(B, max_rank) + x_planes_bytes(B, H, x_dtype) + part_bytes(B, H, O, 1);
+    return v_bytes(B, max_rank) + x_planes_bytes(B, H, x_dtype) + part_bytes(B, H, O, 1, max_rank);
 }
 
 // v of gate, up and down, the planes of x, h (bf16, or three planes for an
@@ -1090,7 +1151,7 @@ size_t lora_workspace_bytes(int B, int H, int O, int max_rank, int x_dtype) {
 size_t shared_ffn_workspace_bytes(int B, int H, int I, int max_rank, int x_dtype, int y_dtype) {
     return 3 * v_bytes(B, max_rank) + x_planes_bytes(B, H, x_dtype) +
            (y_dtype == MOE_DT_F32 ? 3 : 1) * up256(static_cast<size_t>(B) * I * 2) +
-           std::max(part_bytes(B, H, I, 2), part_bytes(B, I, H, 1));
+           std::max(part_bytes(B, H, I, 2, max_rank), part_bytes(B, I, H, 1, max_rank));
 }
 
 hipError_t launch_lora_linear(ProjArgs a, void* ws, hipStream_t s) {
