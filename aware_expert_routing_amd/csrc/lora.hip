@@ -762,18 +762,23 @@ __global__ __launch_bounds__(kFinishWaves* kWave) void proj_finish_kernel(ProjAr
 // Tiled projection, for many tokens: a workgroup of WR x WC waves owns
 // 16 WR MB rows of W (for NM = 2 half of them gate rows and half the up rows of
 // the same outputs) and 16 WC NB tokens; a wave owns MB x NB blocks of 16 x 16
-// in accumulators.  Column tiles go to LDS in operand order (a packed weight
-// tile as it lies; of x the lane's 16 bytes of its token's row), straight from
-// memory (global_load_lds), kStages of them in a ring.
-//   Step s: wait until this wave's copies of step s + 1 have landed (those of
-//   step s + 2 stay in flight); barrier; start the copies of step s + 3 into the
-//   place of step s - 1, whose operands every wave has used by then; read the
-//   operands of step s + 1 while the products of step s run: x into a second
-//   set of registers, each row of W into the registers its last product has
-//   just left.  (The scheduling barriers keep that order: left to itself the
-//   compiler gathers the reads and waits for each.)
-// Steps past the last copy the last one again, so that the waits count alike;
-// nothing reads those.
+// in accumulators.  Operands go to LDS straight from memory (buffer loads to
+// LDS): packed weight tiles as they lie, a ring of kWRing steps of 32 columns;
+// rows of x as whole 128-byte lines, a ring of kXRing pairs of steps.  (Loading
+// x in operand order, 16 bytes from each of 16 rows, touches eight times the
+// lines and cost 16 of 127 us at 4096 tokens of 4096 x 4096.)  In LDS the 16-byte
+// chunk c of row r lies at place c ^ (r / 2 mod 8) of the row, so that the 16
+// rows an operand read takes a chunk from lie in different banks.
+//   Step s: wait until this wave's copies up to those of step s - 2 have
+//   landed, with them the operands of step s + 1; barrier; start the copies of
+//   weight step s + 3 and of half a pair of x, into places whose operands every
+//   wave has used by then; read the operands of step s + 1 while the products
+//   of step s run: x into a second set of registers, each row of W into the
+//   registers its last product has just left.  Copies and reads go between the
+//   products; the scheduling barriers keep them there (left to itself the
+//   compiler gathers the reads and waits for each).
+// Copies past the end take the last step again, so that the waits count alike;
+// nothing uses those.
 // ---------------------------------------------------------------------------
 typedef __attribute__((address_space(3))) void* lptr;
 
@@ -795,7 +800,7 @@ __device__ __forceinline__ void copy_tile(const char* base, int lane_offset, int
 #endif
 }
 
-constexpr int kStages = 4;
+constexpr int kWRing = 4, kXRing = 3;
 
 // At most N vector-memory operations of this wave still in flight; then the
 // workgroup's barrier.
@@ -807,12 +812,14 @@ __device__ __forceinline__ void wait_and_barrier() {
 template <int XK, int YK, int NM, int WR, int WC, int MB, int NB>
 __global__ __launch_bounds__(WR* WC* kWave) void proj_tile_kernel(ProjArgs a, int row_tiles, int tok_tiles) {
     constexpr int NW = WR * WC;
-    constexpr int RT = WR * MB, CT = WC * NB;      // 1 KB tiles per step of 32 columns
-    constexpr int kStep = RT + CT;
-    constexpr int kPer = kStep / NW;               // tiles a wave copies per step
-    static_assert(kStep % NW == 0 && MB % NM == 0 && NB % 4 == 0, "tile split");
+    constexpr int RT = WR * MB, CT = WC * NB;         // row and token blocks of the workgroup
+    constexpr int kPerW = RT / NW, kPerX = CT / NW;   // KB a wave copies per step (of x: kPerX in each step of a pair)
+    constexpr int kPer = kPerW + kPerX;
+    static_assert(RT % NW == 0 && CT % NW == 0 && MB % NM == 0 && NB % 4 == 0 && MB % kPer == 0, "tile split");
     constexpr int P = XK == kActPlanes ? 3 : 1;
-    __shared__ __align__(1024) char lds[kStages * kStep * 1024];
+    constexpr int kXPair = 2 * CT * 1024;
+    __shared__ __align__(1024) char lds[kWRing * RT * 1024 + kXRing * kXPair];
+    char* const lds_x = lds + kWRing * RT * 1024;
     const int lane = threadIdx.x & (kWave - 1);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int n = lane & 15, q = lane >> 4;
@@ -826,40 +833,41 @@ __global__ __launch_bounds__(WR* WC* kWave) void proj_tile_kernel(ProjArgs a, in
     const int tile_r = 4 * band + in % wide, tile_c = in / wide;
     const int i0 = tile_c * 16 * CT;
     if (i0 >= B_real) return;
-    const int blocks = a.O / 16, S = a.H / 32, steps = P * S;
+    const int blocks = a.O / 16, S = a.H / 32;
     const int ob0 = tile_r * (RT / NM);
     // output row block and matrix of row tile j of the workgroup
     constexpr int kHalf = MB / NM;
     auto mat_of = [](int j) { return NM == 1 ? 0 : (j % MB) / kHalf; };
     auto ob_of = [&](int j) { return min(ob0 + (NM == 1 ? j : (j / MB) * kHalf + j % kHalf), blocks - 1); };
 
-    // a tile's base (the same for the wavefront), the lane's offset from it, and the offset of a step
-    const char* base[kPer];
-    int offset[kPer];
+    const char* w_base[kPerW];
 #pragma unroll
-    for (int u = 0; u < kPer; ++u) {
-        const int j = wave * kPer + u;
-        if (j < RT) {
-            base[u] = static_cast<const char*>(mat_of(j) ? a.w[1] : a.w[0]) + static_cast<size_t>(ob_of(j)) * S * 1024;
-            offset[u] = lane * 16;
-        } else {
-            const int i = i0 + 16 * (j - RT);   // (at most 256 rows of 32 KB behind i0)
-            base[u] = static_cast<const char*>(a.x) + static_cast<size_t>(i0) * a.H * 2;
-            offset[u] = (min(i + n, B_real - 1) - i0) * a.H * 2 + 16 * q;
-        }
-        base[u] = uniform(base[u]);
+    for (int u = 0; u < kPerW; ++u) {
+        const int j = wave * kPerW + u;
+        w_base[u] = uniform(static_cast<const char*>(mat_of(j) ? a.w[1] : a.w[0]) +
+                            static_cast<size_t>(ob_of(j)) * S * 1024);
     }
-    auto copy = [&](int step) {
-        const int kk = min(step, steps - 1);
-        const int plane = P == 1 ? 0 : P - 1 - kk / S;   // the smallest term first
-        const int s = P == 1 ? kk : kk % S;
-        char* to = lds + (step % kStages) * kStep * 1024;
+    // x: copy g of a pair takes 8 rows of 128 bytes, lane l chunk (l % 8 ^ swizzle) of row 8 g + l / 8
+    const char* x_base = uniform(static_cast<const char*>(a.x) + static_cast<size_t>(i0) * a.H * 2);
+    int x_at[2][kPerX], x_chunk[2][kPerX];
 #pragma unroll
-        for (int u = 0; u < kPer; ++u) {
-            const int j = wave * kPer + u;
-            const char* from = P == 1 || j < RT ? base[u] : base[u] + static_cast<size_t>(plane) * a.x_plane;
-            copy_tile(from, offset[u], s * (j < RT ? 1024 : 64), to + j * 1024);
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int u = 0; u < kPerX; ++u) {
+            const int r = 8 * ((2 * wave + h) * kPerX + u) + (lane >> 3);   // row of the workgroup's tokens
+            x_chunk[h][u] = (lane & 7) ^ ((r >> 1) & 7);
+            x_at[h][u] = (min(i0 + r, B_real - 1) - i0) * a.H * 2 + 16 * x_chunk[h][u];   // (at most 256 rows of 32 KB)
         }
+    auto copy_w = [&](int step, int u) {
+        copy_tile(w_base[u], lane * 16, min(step, S - 1) * 1024,
+                  lds + (step % kWRing) * RT * 1024 + (wave * kPerW + u) * 1024);
+    };
+    const int last_pair = (S - 1) / 2;
+    auto copy_x = [&](int pair, int place, int h, int u) {
+        // (the last pair of an odd number of steps is half a line)
+        const int back = pair >= last_pair && (S & 1) && x_chunk[h][u] >= 4 ? 64 : 0;
+        copy_tile(x_base, x_at[h][u] - back, min(pair, last_pair) * 128,
+                  lds_x + place * kXPair + ((2 * wave + h) * kPerX + u) * 1024);
     };
 
     constexpr int Q = NB / 4;   // runs of 64 tokens
@@ -870,39 +878,68 @@ __global__ __launch_bounds__(WR* WC* kWave) void proj_tile_kernel(ProjArgs a, in
         for (int j = 0; j < MB; ++j)
 #pragma unroll
             for (int t = 0; t < 4; ++t) acc[h][j][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-    for (int s = 0; s < kStages - 1; ++s) copy(s);
-    wait_and_barrier<kPer*(kStages - 2)>();
     const char* mine_w = lds + wr * MB * 1024 + lane * 16;
-    const char* mine_x = lds + (RT + wc * NB) * 1024 + lane * 16;
-    u32x4 w[MB], x0[NB], x1[NB];
+    const char* mine_x[2];   // by the step's place in its pair
 #pragma unroll
-    for (int t = 0; t < NB; ++t) x0[t] = *reinterpret_cast<const u32x4*>(mine_x + t * 1024);
+    for (int h = 0; h < 2; ++h)
+        mine_x[h] = lds_x + wc * NB * 2048 + n * 128 + (((4 * h + q) ^ ((n >> 1) & 7)) * 16);
+
+    for (int plane = P - 1; plane >= 0; --plane) {   // the smallest term first
+        if (P > 1)
+            x_base = uniform(static_cast<const char*>(a.x) + static_cast<size_t>(plane) * a.x_plane +
+                             static_cast<size_t>(i0) * a.H * 2);
+        int p0 = 0, p1 = 1, p2 = 2;   // places of pairs p, p + 1, p + 2
 #pragma unroll
-    for (int j = 0; j < MB; ++j) w[j] = *reinterpret_cast<const u32x4*>(mine_w + j * 1024);
-    auto step = [&](int s, const u32x4 (&x)[NB], u32x4 (&xn)[NB]) {
-        wait_and_barrier<kPer*(kStages - 3)>();
-        copy(s + kStages - 1);
-        __builtin_amdgcn_sched_barrier(0);
-        const int next = ((s + 1) % kStages) * kStep * 1024;
+        for (int u = 0; u < 2 * kPerX; ++u) copy_x(0, 0, u / kPerX, u % kPerX);
 #pragma unroll
-        for (int j = 0; j < MB; ++j) {
+        for (int u = 0; u < 2 * kPerW; ++u) copy_w(u / kPerW, u % kPerW);
 #pragma unroll
-            for (int t = j * NB / MB; t < (j + 1) * NB / MB; ++t)
-                xn[t] = *reinterpret_cast<const u32x4*>(mine_x + next + t * 1024);
+        for (int u = 0; u < 2 * kPerX; ++u) copy_x(1, 1, u / kPerX, u % kPerX);
 #pragma unroll
-            for (int t = 0; t < NB; ++t) acc[t / 4][j][t % 4] = mma32(w[j], x[t], acc[t / 4][j][t % 4]);
-            w[j] = *reinterpret_cast<const u32x4*>(mine_w + next + j * 1024);
+        for (int u = 0; u < kPerW; ++u) copy_w(2, u);
+        wait_and_barrier<2 * kPerX + 2 * kPerW>();   // pair 0 and weight step 0 are there
+        u32x4 w[MB], x0[NB], x1[NB];
+#pragma unroll
+        for (int t = 0; t < NB; ++t) x0[t] = *reinterpret_cast<const u32x4*>(mine_x[0] + t * 2048);
+#pragma unroll
+        for (int j = 0; j < MB; ++j) w[j] = *reinterpret_cast<const u32x4*>(mine_w + j * 1024);
+        // step s, the h-th of its pair: x_next holds the pair that step s + 1 is in
+        auto step = [&](int s, int h, int x_next, const u32x4 (&x)[NB], u32x4 (&xn)[NB]) {
+            wait_and_barrier<kPer>();
             __builtin_amdgcn_sched_barrier(0);
+            const char* from_w = mine_w + ((s + 1) % kWRing) * RT * 1024;
+            const char* from_x = mine_x[h ^ 1] + x_next * kXPair;
+#pragma unroll
+            for (int j = 0; j < MB; ++j) {
+#pragma unroll
+                for (int t = j * NB / MB; t < (j + 1) * NB / MB; ++t)
+                    xn[t] = *reinterpret_cast<const u32x4*>(from_x + t * 2048);
+#pragma unroll
+                for (int t = 0; t < NB; ++t) acc[t / 4][j][t % 4] = mma32(w[j], x[t], acc[t / 4][j][t % 4]);
+                w[j] = *reinterpret_cast<const u32x4*>(from_w + j * 1024);
+                if (j % (MB / kPer) == MB / kPer - 1) {
+                    const int u = j / (MB / kPer);
+                    if (u < kPerW) copy_w(s + 3, u);
+                    else copy_x(s / 2 + 2, p2, h, u - kPerW);
+                }
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        };
+        for (int s = 0; s + 1 < S; s += 2) {
+            step(s, 0, p0, x0, x1);
+            step(s + 1, 1, p1, x1, x0);
+            const int p = p0;
+            p0 = p1;
+            p1 = p2;
+            p2 = p;
         }
-    };
-    int s = 0;
-    for (; s + 1 < steps; s += 2) {
-        step(s, x0, x1);
-        step(s + 1, x1, x0);
+        if (S & 1)
+#pragma unroll
+            for (int j = 0; j < MB; ++j)
+#pragma unroll
+                for (int t = 0; t < NB; ++t) acc[t / 4][j][t % 4] = mma32(w[j], x0[t], acc[t / 4][j][t % 4]);
+        wait_and_barrier<0>();   // no copy may land in the next plane's ring, or after the workgroup's end
     }
-    if (s < steps) step(s, x0, x1);
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // no copy may land after the workgroup's end
 #pragma unroll
     for (int h = 0; h < Q; ++h) {
         const int i1 = i0 + 16 * NB * wc + 64 * h;
