@@ -20,7 +20,6 @@
 #include "internal.h"
 
 #include <algorithm>
-#include <cstdlib>
 
 namespace moe {
 namespace {
@@ -112,6 +111,48 @@ struct Frag<kActPlanes> {
         for (int i = 0; i < 3; ++i) t[i] = raw[i];
     }
 };
+// The fragments of a pair of column tiles for NT tiles of 16 tokens, loaded as
+// whole lines: a fragment takes 16 bytes from each of 16 rows, and a load that
+// does so touches eight times the cache lines of one in which eight lanes take
+// a row's 128 bytes.  Lane l loads chunk l % 8 of row 8 h + l / 8; the wave turns
+// that into fragments through 2 KB of LDS per tile that it alone uses (LDS
+// operations of a wave stay in order, so nothing is waited for but the data).
+// Chunk c of row r lies at place c ^ (r / 2 mod 8), so that 16 rows' chunks lie
+// in different banks.  bf16 rows and planes; fp32 rows are read as fragments.
+template <int XK, int NT>
+struct Lines {
+    static constexpr int kParts = XK == kActPlanes ? 3 : 1;
+    u32x4 v[NT][2][kParts];
+    // rows: byte offsets of the lane's rows from x
+    __device__ __forceinline__ void load(const ProjArgs& a, const uint32_t (&rows)[NT][2], int pair) {
+        const char* x = static_cast<const char*>(a.x) + static_cast<size_t>(pair) * 128;
+#pragma unroll
+        for (int k = 0; k < kParts; ++k)
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    v[t][h][k] = *reinterpret_cast<const u32x4*>(x + k * a.x_plane + rows[t][h]);
+    }
+    // Part k's fragments of both column tiles: frag[h][t].
+    __device__ __forceinline__ void turn(char* lds, int k, u32x4 (&frag)[2][NT]) const {
+        const int lane = threadIdx.x & (kWave - 1), n = lane & 15, q = lane >> 4;
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int r = 8 * h + (lane >> 3);
+                *reinterpret_cast<u32x4*>(lds + t * 2048 + r * 128 + (((lane & 7) ^ ((r >> 1) & 7)) * 16)) = v[t][h][k];
+            }
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                frag[h][t] = *reinterpret_cast<const u32x4*>(lds + t * 2048 + n * 128 +
+                                                             (((4 * h + q) ^ ((n >> 1) & 7)) * 16));
+    }
+};
+
 // Row i of x, the lane's part of it.
 template <int XK>
 __device__ __forceinline__ const char* x_row(const ProjArgs& a, int i, int q) {
@@ -146,7 +187,10 @@ constexpr int kChunk = 2048;
 
 template <int NT, int RBN, int W>
 struct ShrinkLds {
-    f32x4 part[W / 2][RBN * NT][kWave];
+    union {
+        f32x4 part[W / 2][RBN * NT][kWave];
+        char lines[W][NT * 2048];
+    };
     int tok[16 * NT];
     int found[kChunk / kWave];
 };
@@ -236,12 +280,47 @@ __device__ __forceinline__ void shrink_block(const ProjArgs& a, ShrinkLds<NT, RB
         constexpr int kLoads = 2 * (RBN + NT * (XK == kActF32 ? 2 : Frag<XK>::kTerms));
         constexpr int kU = kLoads >= 12 ? 1 : (kLoads > 6 ? 2 : 4);
         const int pairs = S / 2;
+        if constexpr (XK == kActF32) {
 #pragma unroll kU
-        for (int s = wave; s < pairs; s += W) {
-            tile(2 * s);
-            tile(2 * s + 1);
+            for (int s = wave; s < pairs; s += W) {
+                tile(2 * s);
+                tile(2 * s + 1);
+            }
+        } else {
+            uint32_t rows[NT][2];   // from the chunk's first token
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+                    rows[t][k] = static_cast<uint32_t>(l.tok[min(16 * t + 8 * k + (lane >> 3), have - 1)] - c0) *
+                                     (a.H * 2) + (lane & 7) * 16;
+            ProjArgs c = a;
+            c.x = static_cast<const char*>(a.x) + static_cast<size_t>(c0) * a.H * 2;
+#pragma unroll kU
+            for (int s = wave; s < pairs; s += W) {
+                u32x4 w[2][RBN];
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+#pragma unroll
+                    for (int r = 0; r < RBN; ++r)
+                        w[k][r] = *reinterpret_cast<const u32x4*>(A[r] + static_cast<size_t>(2 * s + k) * 1024);
+                Lines<XK, NT> x;
+                x.load(c, rows, s);
+#pragma unroll
+                for (int k = Lines<XK, NT>::kParts - 1; k >= 0; --k) {
+                    u32x4 f[2][NT];
+                    x.turn(l.lines[wave], k, f);
+#pragma unroll
+                    for (int t = 0; t < NT; ++t)
+#pragma unroll
+                        for (int r = 0; r < RBN; ++r)
+#pragma unroll
+                            for (int g = 0; g < 2; ++g) acc[r * NT + t] = mma32(w[g][r], f[g][t], acc[r * NT + t]);
+                }
+            }
         }
         if ((S & 1) && wave == W - 1) tile(S - 1);
+        __syncthreads();   // the lines' room becomes the sums'
         fold_waves<W>(l.part, acc, wave, lane);
         for (int p = wave; p < RBN * NT; p += W) {
             const int r = p / NT, t = p % NT;
@@ -592,6 +671,7 @@ __global__ __launch_bounds__(kSplitWaves* kWave) void proj_split_kernel(ProjArgs
     constexpr int SNT = NT == 1 ? 1 : 2;
     union Lds {
         f32x4 part[W / 2][T][kWave];
+        char lines[W][NT * 2048];
         ShrinkLds<SNT, 1, W> shrink;
     };
     __shared__ Lds l;
@@ -647,16 +727,51 @@ __global__ __launch_bounds__(kSplitWaves* kWave) void proj_split_kernel(ProjArgs
                 for (int j = 0; j < MB; ++j) acc[j * NT + t] = mma32(w[j], x[k], acc[j * NT + t]);
         }
     };
-    if (s1 - s0 >= 2 * W) {   // pairs of tiles: one 128-byte line of a bf16 row
+    if (s1 - s0 >= 2 * W || XK == kActF32) {
         const int pairs = (s1 - s0) / 2;
         constexpr int kU = T * TT > 8 ? 1 : 2;
+        if constexpr (XK == kActF32) {
 #pragma unroll kU
-        for (int p = wave; p < pairs; p += W) {
-            tile(s0 + 2 * p);
-            tile(s0 + 2 * p + 1);
+            for (int p = wave; p < pairs; p += W) {
+                tile(s0 + 2 * p);
+                tile(s0 + 2 * p + 1);
+            }
+        } else {
+            uint32_t rows[NT][2];   // from the group's first token
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+                    rows[t][k] = static_cast<uint32_t>(min(16 * t + 8 * k + (lane >> 3), B_real - 1 - i0)) * (a.H * 2) +
+                                 (lane & 7) * 16;
+            ProjArgs c = a;
+            c.x = static_cast<const char*>(a.x) + static_cast<size_t>(i0) * a.H * 2 + static_cast<size_t>(s0) * 64;
+#pragma unroll kU
+            for (int p = wave; p < pairs; p += W) {
+                u32x4 w[2][MB];
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+#pragma unroll
+                    for (int j = 0; j < MB; ++j)
+                        w[k][j] = *reinterpret_cast<const u32x4*>(wp[j] + static_cast<size_t>(s0 + 2 * p + k) * 1024);
+                Lines<XK, NT> x;
+                x.load(c, rows, p);
+#pragma unroll
+                for (int k = Lines<XK, NT>::kParts - 1; k >= 0; --k) {
+                    u32x4 f[2][NT];
+                    x.turn(l.lines[wave], k, f);
+#pragma unroll
+                    for (int t = 0; t < NT; ++t)
+#pragma unroll
+                        for (int j = 0; j < MB; ++j)
+#pragma unroll
+                            for (int g = 0; g < 2; ++g) acc[j * NT + t] = mma32(w[g][j], f[g][t], acc[j * NT + t]);
+                }
+            }
         }
         if (((s1 - s0) & 1) && wave == W - 1) tile(s1 - 1);
-    } else {                  // fewer: a tile for every wave first
+        __syncthreads();   // the lines' room becomes the sums'
+    } else {                  // few: a tile for every wave first
         for (int s = s0 + wave; s < s1; s += W) tile(s);
     }
     fold_waves<W>(l.part, acc, wave, lane);
@@ -810,7 +925,7 @@ __device__ __forceinline__ void wait_and_barrier() {
 }
 
 template <int XK, int YK, int NM, int WR, int WC, int MB, int NB>
-__global__ __launch_bounds__(WR* WC* kWave) void proj_tile_kernel(ProjArgs a, int row_tiles, int tok_tiles) {
+__global__ __launch_bounds__(WR* WC* kWave, 2) void proj_tile_kernel(ProjArgs a, int row_tiles, int tok_tiles) {
     constexpr int NW = WR * WC;
     constexpr int RT = WR * MB, CT = WC * NB;         // row and token blocks of the workgroup
     constexpr int kPerW = RT / NW, kPerX = CT / NW;   // KB a wave copies per step (of x: kPerX in each step of a pair)
@@ -1009,8 +1124,9 @@ Plan plan_proj(int B, int H, int O, int mats, int rank_blocks) {
     SplitArgs& g = p.split;
     g.row_groups = (blocks + p.rb - 1) / p.rb;
     g.tok_groups = (B + 16 * p.nt - 1) / (16 * p.nt);
-    // two workgroups per compute unit, but at least a pair of tiles per wave
-    const int want = std::max(1, (getenv("KW") ? atoi(getenv("KW")) : 512) / (g.row_groups * g.tok_groups));
+    // a workgroup per compute unit (two: 14.4 against 11.6 us for 64 tokens of 4096 x 4096, more partial
+    // blocks to write and add), but at least a pair of tiles per wave
+    const int want = std::max(1, 256 / (g.row_groups * g.tok_groups));
     const int most = std::max(1, S / (2 * kSplitWaves));
     g.parts = std::min(want, most);
     g.steps = (S + g.parts - 1) / g.parts;
