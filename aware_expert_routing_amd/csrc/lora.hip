@@ -276,7 +276,7 @@ __device__ __forceinline__ void shrink_block(const ProjArgs& a, ShrinkLds<NT, RB
                     for (int r = 0; r < RBN; ++r) acc[r * NT + t] = mma32(w[r], x[k], acc[r * NT + t]);
             }
         };
-        // about 24 loads of a wave in flight
+        // kU pairs of a wave in flight: about 24 loads
         constexpr int kLoads = 2 * (RBN + NT * (XK == kActF32 ? 2 : Frag<XK>::kTerms));
         constexpr int kU = kLoads >= 12 ? 1 : (kLoads > 6 ? 2 : 4);
         const int pairs = S / 2;
@@ -296,26 +296,35 @@ __device__ __forceinline__ void shrink_block(const ProjArgs& a, ShrinkLds<NT, RB
                                      (a.H * 2) + (lane & 7) * 16;
             ProjArgs c = a;
             c.x = static_cast<const char*>(a.x) + static_cast<size_t>(c0) * a.H * 2;
-#pragma unroll kU
-            for (int s = wave; s < pairs; s += W) {
-                u32x4 w[2][RBN];
+            for (int s = wave; s < pairs; s += W * kU) {
+                u32x4 w[kU][2][RBN];
+                Lines<XK, NT> x[kU];
 #pragma unroll
-                for (int k = 0; k < 2; ++k)
+                for (int u = 0; u < kU; ++u) {
+                    const int p = s + u * W;
+                    if (p >= pairs) continue;
 #pragma unroll
-                    for (int r = 0; r < RBN; ++r)
-                        w[k][r] = *reinterpret_cast<const u32x4*>(A[r] + static_cast<size_t>(2 * s + k) * 1024);
-                Lines<XK, NT> x;
-                x.load(c, rows, s);
-#pragma unroll
-                for (int k = Lines<XK, NT>::kParts - 1; k >= 0; --k) {
-                    u32x4 f[2][NT];
-                    x.turn(l.lines[wave], k, f);
-#pragma unroll
-                    for (int t = 0; t < NT; ++t)
+                    for (int k = 0; k < 2; ++k)
 #pragma unroll
                         for (int r = 0; r < RBN; ++r)
+                            w[u][k][r] = *reinterpret_cast<const u32x4*>(A[r] + static_cast<size_t>(2 * p + k) * 1024);
+                    x[u].load(c, rows, p);
+                }
 #pragma unroll
-                            for (int g = 0; g < 2; ++g) acc[r * NT + t] = mma32(w[g][r], f[g][t], acc[r * NT + t]);
+                for (int u = 0; u < kU; ++u) {
+                    if (s + u * W >= pairs) continue;
+#pragma unroll
+                    for (int k = Lines<XK, NT>::kParts - 1; k >= 0; --k) {
+                        u32x4 f[2][NT];
+                        x[u].turn(l.lines[wave], k, f);
+#pragma unroll
+                        for (int t = 0; t < NT; ++t)
+#pragma unroll
+                            for (int r = 0; r < RBN; ++r)
+#pragma unroll
+                                for (int g = 0; g < 2; ++g)
+                                    acc[r * NT + t] = mma32(w[u][g][r], f[g][t], acc[r * NT + t]);
+                    }
                 }
             }
         }
@@ -610,6 +619,10 @@ __global__ __launch_bounds__(W* kWave) void proj_fused_kernel(ProjArgs a) {
 constexpr int kSplitWaves = 8;
 constexpr int kFinishWaves = 8;
 
+__device__ __forceinline__ uint32_t lane_u32(uint32_t v, int l) {
+    return static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(v), l));
+}
+
 // A rank block of one adapter among the tokens of a tile.
 struct RankItem {
     const char* b;   // its half tile of row block 0; row block ob lies ob * nb * 512 further
@@ -746,26 +759,36 @@ __global__ __launch_bounds__(kSplitWaves* kWave) void proj_split_kernel(ProjArgs
                                  (lane & 7) * 16;
             ProjArgs c = a;
             c.x = static_cast<const char*>(a.x) + static_cast<size_t>(i0) * a.H * 2 + static_cast<size_t>(s0) * 64;
-#pragma unroll kU
-            for (int p = wave; p < pairs; p += W) {
-                u32x4 w[2][MB];
+            for (int p = wave; p < pairs; p += W * kU) {
+                u32x4 w[kU][2][MB];
+                Lines<XK, NT> x[kU];
 #pragma unroll
-                for (int k = 0; k < 2; ++k)
+                for (int u = 0; u < kU; ++u) {
+                    const int s = p + u * W;
+                    if (s >= pairs) continue;
 #pragma unroll
-                    for (int j = 0; j < MB; ++j)
-                        w[k][j] = *reinterpret_cast<const u32x4*>(wp[j] + static_cast<size_t>(s0 + 2 * p + k) * 1024);
-                Lines<XK, NT> x;
-                x.load(c, rows, p);
-#pragma unroll
-                for (int k = Lines<XK, NT>::kParts - 1; k >= 0; --k) {
-                    u32x4 f[2][NT];
-                    x.turn(l.lines[wave], k, f);
-#pragma unroll
-                    for (int t = 0; t < NT; ++t)
+                    for (int k = 0; k < 2; ++k)
 #pragma unroll
                         for (int j = 0; j < MB; ++j)
+                            w[u][k][j] =
+                                *reinterpret_cast<const u32x4*>(wp[j] + static_cast<size_t>(s0 + 2 * s + k) * 1024);
+                    x[u].load(c, rows, s);
+                }
 #pragma unroll
-                            for (int g = 0; g < 2; ++g) acc[j * NT + t] = mma32(w[g][j], f[g][t], acc[j * NT + t]);
+                for (int u = 0; u < kU; ++u) {
+                    if (p + u * W >= pairs) continue;
+#pragma unroll
+                    for (int k = Lines<XK, NT>::kParts - 1; k >= 0; --k) {
+                        u32x4 f[2][NT];
+                        x[u].turn(l.lines[wave], k, f);
+#pragma unroll
+                        for (int t = 0; t < NT; ++t)
+#pragma unroll
+                            for (int j = 0; j < MB; ++j)
+#pragma unroll
+                                for (int g = 0; g < 2; ++g)
+                                    acc[j * NT + t] = mma32(w[u][g][j], f[g][t], acc[j * NT + t]);
+                    }
                 }
             }
         }
@@ -790,7 +813,7 @@ __global__ __launch_bounds__(kSplitWaves* kWave) void proj_split_kernel(ProjArgs
 template <int YK, int NM, int RBF>
 __global__ __launch_bounds__(kFinishWaves* kWave) void proj_finish_kernel(ProjArgs a, SplitArgs g) {
     constexpr int W = kFinishWaves, VT = v_terms_for<YK>(), T = NM * RBF;
-    constexpr int D = 2;   // rank blocks in flight per matrix
+    constexpr int D = 4;   // rank blocks in flight per matrix
     __shared__ f32x4 part[W / 2][T][kWave];
     const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
     const int n = lane & 15, q = lane >> 4;
@@ -808,12 +831,13 @@ __global__ __launch_bounds__(kFinishWaves* kWave) void proj_finish_kernel(ProjAr
                               min(ob0 + p % RBF, blocks - 1)) * kWave + lane];
     if (g.list_wgs > 0) {
         const size_t row = static_cast<size_t>(min(i, B_real - 1)) * a.max_rank;
-        const RankItem* items[NM];
+        // lane l holds the wave's item l: one load for the whole list
+        u32x4 items[NM];
         int count[NM], most = 0;
 #pragma unroll
         for (int m = 0; m < NM; ++m) {
             const size_t at = (static_cast<size_t>(m) * tt_all + tt) * W + __builtin_amdgcn_readfirstlane(wave);
-            items[m] = g.items + at * kMaxItems;
+            items[m] = *reinterpret_cast<const u32x4*>(g.items + at * kMaxItems + min(lane, kMaxItems - 1));
             count[m] = g.n_items[at];
             most = max(most, count[m]);
         }
@@ -827,7 +851,11 @@ __global__ __launch_bounds__(kFinishWaves* kWave) void proj_finish_kernel(ProjAr
                 for (int d = 0; d < D; ++d) {
                     who[m][d] = 0u;
                     if (d0 + d >= count[m]) continue;
-                    const RankItem it = items[m][d0 + d];
+                    RankItem it;
+                    const uint32_t words[4] = {lane_u32(items[m].x, d0 + d), lane_u32(items[m].y, d0 + d),
+                                               lane_u32(items[m].z, d0 + d), lane_u32(items[m].w, d0 + d)};
+                    static_assert(sizeof(it) == sizeof(words), "an item is 16 bytes");
+                    __builtin_memcpy(&it, words, sizeof(it));
                     who[m][d] = it.who;
 #pragma unroll
                     for (int j = 0; j < RBF; ++j)
