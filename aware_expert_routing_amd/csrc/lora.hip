@@ -209,8 +209,8 @@ __device__ __forceinline__ void fold_waves(f32x4 (*part)[T][kWave], const f32x4 
     __syncthreads();
 }
 
-// Parts first_part, first_part + step, .. (step 0: that part alone) of adapter
-// ad's tokens, rank blocks rb0 .. of table t_id; c1 - c0 <= kChunk.
+// Parts first_part, first_part + step, .. of adapter ad's tokens, rank blocks
+// rb0 .. of table t_id; c1 - c0 <= kChunk.
 template <int XK, int NT, int RBN, int W>
 __device__ __forceinline__ void shrink_block(const ProjArgs& a, ShrinkLds<NT, RBN, W>& l, int t_id, int ad, int rb0,
                                              int c0, int c1, int first_part, int step) {
@@ -340,7 +340,6 @@ __device__ __forceinline__ void shrink_block(const ProjArgs& a, ShrinkLds<NT, RB
             float* out = a.v[t_id] + static_cast<size_t>(l.tok[16 * t + n]) * a.max_rank + 16 * (rb0 + r) + 4 * q;
             *reinterpret_cast<f32x4*>(out) = v * h.scale;
         }
-        if (step == 0) return;
         __syncthreads();
     }
 }
@@ -368,77 +367,115 @@ __global__ __launch_bounds__(W* kWave) void shrink_kernel(ProjArgs a, int parts,
     const int c0 = (blockIdx.y / parts) * kChunk, c1 = min(c0 + kChunk, real_tokens(a));
     if (a.table[t_id] == nullptr || c0 >= c1) return;
     const int ad = shrink_adapter(a, blockIdx.x, by_token, c0, c1);
-    if (ad >= 0) shrink_block<XK, NT, RBN, W>(a, l, t_id, ad, rb0, c0, c1, blockIdx.y % parts, 0);
+    if (ad >= 0) shrink_block<XK, NT, RBN, W>(a, l, t_id, ad, rb0, c0, c1, blockIdx.y % parts, parts);
 }
 
-// Rank block r of the lane's token's v as bf16 terms (zero where !mine).
-template <int VT>
-__device__ __forceinline__ void v_terms(const float* v_row, int r, int q, bool mine, u32x2 (&out)[VT]) {
-    f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
-    if (mine) v = *reinterpret_cast<const f32x4*>(v_row + 16 * r + 4 * q);
-    const float f[4] = {v.x, v.y, v.z, v.w};
-    uint32_t t[VT][2];
-    split<VT, 2>(f, t);
-#pragma unroll
-    for (int k = 0; k < VT; ++k) out[k] = u32x2{t[k][0], t[k][1]};
+__device__ __forceinline__ uint32_t lane_u32(uint32_t v, int l) {
+    return static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(v), l));
 }
 
-// Adds B_a v to the accumulators of MB row blocks and NB tiles of 16 tokens
-// (i0 the first token), one adapter of those tokens after the other.  ob(j):
+// Adds B_a v to the accumulators of MB row blocks (of NM matrices) and 64
+// tokens (i0 the first), one rank block of one adapter after the other; the
+// next one's operands are loaded before the present one's products.  ob(j):
 // row block of accumulator row j, mat(j): its matrix.
-template <int VT, int MB, int NB, typename Ob, typename Mat>
-__device__ __forceinline__ void expand(const ProjArgs& a, int i0, int B_real, f32x4 (&acc)[MB][NB], Ob ob,
-                                       Mat mat) {
-    static_assert(NB <= 4, "a token per lane");
+template <int VT, int NM, int MB, typename Ob, typename Mat>
+__device__ __forceinline__ void expand(const ProjArgs& a, int i0, int B_real, f32x4 (&acc)[MB][4], Ob ob, Mat mat) {
     if (a.adapter == nullptr) return;
     const int lane = threadIdx.x & (kWave - 1), n = lane & 15, q = lane >> 4;
-    const int id = lane < 16 * NB ? adapter_of(a, i0 + lane, B_real) : -1;   // lane = token
-    uint64_t rem = __ballot(id >= 0);
-    while (rem != 0ull) {
-        const int ad = __builtin_amdgcn_readlane(id, __ffsll(static_cast<unsigned long long>(rem)) - 1);
-        const uint64_t who = __ballot(id == ad);
-        rem &= ~who;
-        constexpr bool kTwo = MB > 1;
-        moe_lora_handle h[2];
-        int nb[2] = {0, 0};
+    const int id = adapter_of(a, i0 + lane, B_real);   // lane = token
+    // every lane reads its own token's handles, all of them in one round trip
+    int nb[NM];
+    uint64_t hb[NM];
 #pragma unroll
-        for (int m = 0; m < (kTwo ? 2 : 1); ++m)
-            if (a.table[m] != nullptr) {
-                h[m] = a.table[m][ad];
-                nb[m] = rank_blocks(h[m], a.max_rank);
+    for (int m = 0; m < NM; ++m) {
+        nb[m] = 0;
+        hb[m] = 0;
+        if (a.table[m] != nullptr && id >= 0) {
+            const moe_lora_handle* h = a.table[m] + id;
+            nb[m] = rank_blocks(*h, a.max_rank);
+            hb[m] = reinterpret_cast<uint64_t>(h->b);
+        }
+    }
+    bool any = nb[0] > 0;
+    if constexpr (NM == 2) any = any || nb[1] > 0;
+    uint64_t rem = __ballot(any);
+    struct Item {
+        uint64_t who;
+        const char* b[NM];
+        int nb[NM], r;
+    } cur{}, nxt{};
+    nxt.r = -1;
+    auto next = [&](Item& it) {   // the rank block after `it`, false: none
+        int most = it.nb[0];
+        if constexpr (NM == 2) most = max(most, it.nb[1]);
+        if (++it.r < most) return true;
+        if (rem == 0ull) return false;
+        const int from = __ffsll(static_cast<unsigned long long>(rem)) - 1;
+        const int ad = __builtin_amdgcn_readlane(id, from);
+        it.who = __ballot(id == ad);
+        rem &= ~it.who;
+        it.r = 0;
+#pragma unroll
+        for (int m = 0; m < NM; ++m) {
+            it.nb[m] = __builtin_amdgcn_readlane(nb[m], from);
+            it.b[m] = reinterpret_cast<const char*>(
+                (static_cast<uint64_t>(lane_u32(static_cast<uint32_t>(hb[m] >> 32), from)) << 32) |
+                lane_u32(static_cast<uint32_t>(hb[m]), from));
+        }
+        return true;
+    };
+    auto load = [&](const Item& it, u32x2 (&b)[MB], f32x4 (&v)[NM][4]) {
+#pragma unroll
+        for (int j = 0; j < MB; ++j) {
+            const int m = mat(j);
+            b[j] = u32x2{0u, 0u};
+            if (it.r < it.nb[m])
+                b[j] = *reinterpret_cast<const u32x2*>(it.b[m] + (static_cast<size_t>(ob(j)) * it.nb[m] + it.r) * 512 +
+                                                       lane * 8);
+        }
+#pragma unroll
+        for (int m = 0; m < NM; ++m)
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                v[m][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+                if (((it.who >> (16 * t + n)) & 1ull) && it.r < it.nb[m])
+                    v[m][t] = *reinterpret_cast<const f32x4*>(
+                        a.v[m] + static_cast<size_t>(i0 + 16 * t + n) * a.max_rank + 16 * it.r + 4 * q);
             }
-        const int most = max(nb[0], nb[1]);
-        for (int r = 0; r < most; ++r) {
-            u32x2 b[MB];
+    };
+    u32x2 b0[MB], b1[MB];
+    f32x4 v0[NM][4], v1[NM][4];
+    bool more = next(nxt);
+    if (more) load(nxt, b0, v0);
+    while (more) {
+        cur = nxt;
+        more = next(nxt);
+        if (more) load(nxt, b1, v1);
 #pragma unroll
-            for (int j = 0; j < MB; ++j) {
-                const int m = mat(j);
-                b[j] = u32x2{0u, 0u};
-                if (r < nb[m])
-                    b[j] = *reinterpret_cast<const u32x2*>(static_cast<const char*>(h[m].b) +
-                                                           (static_cast<size_t>(ob(j)) * nb[m] + r) * 512 + lane * 8);
-            }
+        for (int t = 0; t < 4; ++t) {
+            if (((cur.who >> (16 * t)) & 0xffffull) == 0ull) continue;
+            const bool mine = (cur.who >> (16 * t + n)) & 1ull;
 #pragma unroll
-            for (int t = 0; t < NB; ++t) {
-                if (((who >> (16 * t)) & 0xffffull) == 0ull) continue;
-                const bool mine = (who >> (16 * t + n)) & 1ull;
-                const size_t row = static_cast<size_t>(min(i0 + 16 * t + n, B_real - 1)) * a.max_rank;
+            for (int m = 0; m < NM; ++m) {
+                const float f[4] = {v0[m][t].x, v0[m][t].y, v0[m][t].z, v0[m][t].w};
+                uint32_t terms[VT][2];
+                split<VT, 2>(f, terms);
 #pragma unroll
-                for (int m = 0; m < (kTwo ? 2 : 1); ++m) {
-                    if (r >= nb[m]) continue;
-                    u32x2 v[VT];
-                    v_terms<VT>(a.v[m] + row, r, q, mine, v);
+                for (int j = 0; j < MB; ++j) {
+                    if (mat(j) != m) continue;
+                    f32x4 sum = acc[j][t];
 #pragma unroll
-                    for (int j = 0; j < MB; ++j) {
-                        if (mat(j) != m) continue;
-                        f32x4 sum = acc[j][t];
-#pragma unroll
-                        for (int k = VT - 1; k >= 0; --k) sum = mma16(b[j], v[k], sum);
-                        acc[j][t] = mine ? sum : acc[j][t];   // (a non-finite B stays with its own tokens)
-                    }
+                    for (int k = VT - 1; k >= 0; --k) sum = mma16(b0[j], u32x2{terms[k][0], terms[k][1]}, sum);
+                    acc[j][t] = mine ? sum : acc[j][t];   // (a non-finite B stays with its own tokens)
                 }
             }
         }
+#pragma unroll
+        for (int j = 0; j < MB; ++j) b0[j] = b1[j];
+#pragma unroll
+        for (int m = 0; m < NM; ++m)
+#pragma unroll
+            for (int t = 0; t < 4; ++t) v0[m][t] = v1[m][t];
     }
 }
 
@@ -618,10 +655,6 @@ __global__ __launch_bounds__(W* kWave) void proj_fused_kernel(ProjArgs a) {
 // ---------------------------------------------------------------------------
 constexpr int kSplitWaves = 8;
 constexpr int kFinishWaves = 8;
-
-__device__ __forceinline__ uint32_t lane_u32(uint32_t v, int l) {
-    return static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(v), l));
-}
 
 // A rank block of one adapter among the tokens of a tile.
 struct RankItem {
@@ -1086,7 +1119,7 @@ __global__ __launch_bounds__(WR* WC* kWave, 2) void proj_tile_kernel(ProjArgs a,
 #pragma unroll
     for (int h = 0; h < Q; ++h) {
         const int i1 = i0 + 16 * NB * wc + 64 * h;
-        expand<v_terms_for<YK>()>(a, i1, B_real, acc[h], [&](int j) { return ob_of(wr * MB + j); },
+        expand<v_terms_for<YK>(), NM>(a, i1, B_real, acc[h], [&](int j) { return ob_of(wr * MB + j); },
                                   [&](int j) { return mat_of(j); });
 #pragma unroll
         for (int j = 0; j < kHalf; ++j) {
@@ -1184,13 +1217,13 @@ void launch_split(const ProjArgs& a, const SplitArgs& g, hipStream_t s) {
 
 template <int XK>
 void launch_shrink(const ProjArgs& a, int tables, hipStream_t s) {
-    constexpr int NT = 2, RBN = 4, W = 16;
+    constexpr int NT = 2, RBN = 2, W = 8;
     const int chunk = std::min(a.B, kChunk), chunks = (a.B + kChunk - 1) / kChunk;
-    const int parts = (chunk + 16 * NT - 1) / (16 * NT);
-    const int by_token = a.n_adapters > chunk;
+    const int by_token = a.n_adapters > chunk, places = by_token ? chunk : a.n_adapters;
+    // workgroups per place: with tokens spread evenly each has a part or two; more tokens take turns
+    const int parts = std::max(1, std::min((chunk + 16 * NT - 1) / (16 * NT), 128 / places));
     const int pieces = (a.max_rank / 16 + RBN - 1) / RBN;
-    shrink_kernel<XK, NT, RBN, W><<<dim3(by_token ? chunk : a.n_adapters, parts * chunks, pieces * tables), W * kWave, 0,
-                                    s>>>(a, parts, by_token);
+    shrink_kernel<XK, NT, RBN, W><<<dim3(places, parts * chunks, pieces * tables), W * kWave, 0, s>>>(a, parts, by_token);
 }
 
 // One projection (NM = 1) or the gate/up pair (NM = 2).
