@@ -673,7 +673,7 @@ struct SplitArgs {
     int* n_items;        // [NM][token tiles][kFinishWaves]
     int parts, steps;    // column tiles per part
     int row_groups, tok_groups;
-    int shrink_wgs, places, by_token;
+    int shrink_wgs, places, shrink_parts, by_token;
     int list_wgs;        // one per matrix and token tile, 0: no adapters
 };
 
@@ -727,10 +727,10 @@ __global__ __launch_bounds__(kSplitWaves* kWave) void proj_split_kernel(ProjArgs
     if (static_cast<int>(blockIdx.x) < g.shrink_wgs) {
         const int pieces = a.max_rank / 16;
         const int at = blockIdx.x % g.places, rest = blockIdx.x / g.places;
-        const int rb = rest % pieces, t_id = rest / pieces;
+        const int first = rest % g.shrink_parts, rb = rest / g.shrink_parts % pieces, t_id = rest / g.shrink_parts / pieces;
         if (a.table[t_id] == nullptr || B_real <= 0) return;
         const int ad = shrink_adapter(a, at, g.by_token, 0, B_real);
-        if (ad >= 0) shrink_block<XK, SNT, 1, W>(a, l.shrink, t_id, ad, rb, 0, B_real, 0, 1);
+        if (ad >= 0) shrink_block<XK, SNT, 1, W>(a, l.shrink, t_id, ad, rb, 0, B_real, first, g.shrink_parts);
         return;
     }
     if (static_cast<int>(blockIdx.x) < g.shrink_wgs + g.list_wgs) {
@@ -1157,8 +1157,6 @@ __global__ __launch_bounds__(256) void planes_kernel(const f32x4* __restrict__ x
 // Which kernels a projection takes, from its sizes alone.
 // ---------------------------------------------------------------------------
 constexpr int kRowTokens = 16;       // up to this many: fp32 rows are cut in registers
-constexpr int kSplitTokens = 256;    // up to this many: the split kernels, above the tiled one
-
 enum Path { kFused, kSplit, kTiled };
 struct Plan {
     Path path;
@@ -1167,15 +1165,12 @@ struct Plan {
     size_t part_bytes, item_bytes, count_bytes;
 };
 
-// rank_blocks: what the batch's adapters may hold together (0: no adapters).
-Plan plan_proj(int B, int H, int O, int mats, int rank_blocks) {
+// rank_blocks: what the batch's adapters may hold together (0: no adapters);
+// terms: bf16 terms an activation enters with.
+Plan plan_proj(int B, int H, int O, int mats, int rank_blocks, int terms) {
     Plan p{};
     if (B <= 16 && rank_blocks <= kFusedBlocks) {
         p.path = kFused;
-        return p;
-    }
-    if (B > kSplitTokens) {
-        p.path = kTiled;
         return p;
     }
     p.path = kSplit;
@@ -1187,12 +1182,29 @@ Plan plan_proj(int B, int H, int O, int mats, int rank_blocks) {
     g.tok_groups = (B + 16 * p.nt - 1) / (16 * p.nt);
     // a workgroup per compute unit (two: 14.4 against 11.6 us for 64 tokens of 4096 x 4096, more partial
     // blocks to write and add), but at least a pair of tiles per wave
-    const int want = std::max(1, 256 / (g.row_groups * g.tok_groups));
+    const long groups = static_cast<long>(g.row_groups) * g.tok_groups;
+    const int want = static_cast<int>(std::max(1L, 256 / groups));
     const int most = std::max(1, S / (2 * kSplitWaves));
     g.parts = std::min(want, most);
     g.steps = (S + g.parts - 1) / g.parts;
     g.steps += g.steps & 1;
     g.parts = (S + g.steps - 1) / g.steps;
+    if (B > 64) {
+        // Split or tiled, by what 96 sizes of H 512-4096, O 256-4096 and B 65-4096 measured, in ns (within 20 %).
+        // Split: 3 us and, for each workgroup on a compute unit, 5.5 us and 127 ns per step of 32 columns
+        // (4096 x 1024, B = 512: 19 us against 35 tiled).  Tiled: 3.3 us and 250 ns per step, which two workgroups
+        // on a unit share well (B = 4096 of the same: 98 split, 39 tiled).  Adapters cost the tiled path a launch
+        // before and the rank blocks behind its products.
+        const long rounds = (groups * g.parts + 255) / 256;
+        const long tiles = (static_cast<long>(O) * mats + 127) / 128 * ((B + 127) / 128);
+        const long split_ns = 3000 + rounds * (5500 + 127L * g.steps * (terms > 1 ? 2 : 1));
+        const long tile_ns = 3300 + 250L * S * terms * std::max(100L, 35 + 65 * tiles / 256) / 100 +
+                             (rank_blocks > 0 ? 6000 : 0);
+        if (B > kChunk || tile_ns < split_ns) {   // (the split launch forms v over one chunk of tokens)
+            p.path = kTiled;
+            return p;
+        }
+    }
     const size_t lists = static_cast<size_t>(mats) * ((B + 15) / 16) * kFinishWaves;
     p.part_bytes = static_cast<size_t>(g.parts) * mats * ((B + 15) / 16) * blocks * 1024;
     p.item_bytes = lists * kMaxItems * sizeof(RankItem);
@@ -1230,7 +1242,8 @@ void launch_shrink(const ProjArgs& a, int tables, hipStream_t s) {
 template <int XK, int YK, int NM>
 hipError_t launch_proj(const ProjArgs& a, void* part, hipStream_t s) {
     const bool lora = a.adapter != nullptr && (a.table[0] != nullptr || (NM == 2 && a.table[1] != nullptr));
-    Plan p = plan_proj(a.B, a.H, a.O, NM, a.adapter != nullptr ? rank_blocks_bound(a.B, a.n_adapters, a.max_rank) : 0);
+    Plan p = plan_proj(a.B, a.H, a.O, NM, a.adapter != nullptr ? rank_blocks_bound(a.B, a.n_adapters, a.max_rank) : 0,
+                       XK == kActBf16 ? 1 : 3);
     if (p.path == kFused) {
         proj_fused_kernel<XK, YK, NM, 8, 4><<<a.O / 16, 8 * kWave, 0, s>>>(a);
         return hipGetLastError();
@@ -1244,7 +1257,9 @@ hipError_t launch_proj(const ProjArgs& a, void* part, hipStream_t s) {
         if (lora) {
             g.by_token = a.n_adapters > a.B;
             g.places = g.by_token ? a.B : a.n_adapters;
-            g.shrink_wgs = g.places * (a.max_rank / 16) * NM;
+            // workgroups per place and rank block: with tokens spread evenly one part each; more tokens take turns
+            g.shrink_parts = std::max(1, std::min((a.B + 31) / 32, 32 / g.places));
+            g.shrink_wgs = g.places * g.shrink_parts * (a.max_rank / 16) * NM;
             g.list_wgs = NM * ((a.B + 15) / 16);
         }
         if (p.nt == 1) launch_split<XK, NM, 1, 2 / NM>(a, g, s);
@@ -1267,8 +1282,10 @@ hipError_t launch_proj(const ProjArgs& a, void* part, hipStream_t s) {
             hipError_t e = hipGetLastError();
             if (e != hipSuccess) return e;
         }
-        const long big = (static_cast<long>(a.O) * NM + 255) / 256 * ((a.B + 255) / 256);
-        return big >= 128 ? launch_tile<XK, YK, NM, 2, 4, 8, 4>(a, s) : launch_tile<XK, YK, NM, 2, 2, 4, 4>(a, s);
+        // 128 x 128 tiles, two workgroups on a compute unit, up to three rounds of units (512 tiles of H = 4096: 65 us
+        // against 83); 256 x 256 beyond (1024: 109 against 130).  The gate/up pair turns earlier (576: 111 against 100).
+        const long tiles = (static_cast<long>(a.O) * NM + 127) / 128 * ((a.B + 127) / 128);
+        return tiles < (NM == 2 ? 576 : 768) ? launch_tile<XK, YK, NM, 2, 2, 4, 4>(a, s) : launch_tile<XK, YK, NM, 2, 4, 8, 4>(a, s);
     }
     return hipErrorInvalidValue;
 }
@@ -1335,8 +1352,8 @@ size_t x_planes_bytes(int B, int H, int x_dtype) {   // fp32 x of more than kRow
 }
 // Partial blocks and item lists of a projection: the most any number of
 // adapters asks for.
-size_t part_bytes(int B, int H, int O, int mats, int max_rank) {
-    const Plan p = plan_proj(B, H, O, mats, max_rank > 0 ? kFusedBlocks + 1 : 0);
+size_t part_bytes(int B, int H, int O, int mats, int max_rank, int x_dtype) {
+    const Plan p = plan_proj(B, H, O, mats, max_rank > 0 ? kFusedBlocks + 1 : 0, x_dtype == MOE_DT_F32 ? 3 : 1);
     return up256(p.part_bytes + p.item_bytes + p.count_bytes);
 }
 
@@ -1357,7 +1374,7 @@ hipError_t cut_x(ProjArgs& a, void* ws, hipStream_t s) {
 
 // v, the planes of x, partial blocks.
 size_t lora_workspace_bytes(int B, int H, int O, int max_rank, int x_dtype) {
-    return v_bytes(B, max_rank) + x_planes_bytes(B, H, x_dtype) + part_bytes(B, H, O, 1, max_rank);
+    return v_bytes(B, max_rank) + x_planes_bytes(B, H, x_dtype) + part_bytes(B, H, O, 1, max_rank, x_dtype);
 }
 
 // v of gate, up and down, the planes of x, h (bf16, or three planes for an
@@ -1365,7 +1382,7 @@ size_t lora_workspace_bytes(int B, int H, int O, int max_rank, int x_dtype) {
 size_t shared_ffn_workspace_bytes(int B, int H, int I, int max_rank, int x_dtype, int y_dtype) {
     return 3 * v_bytes(B, max_rank) + x_planes_bytes(B, H, x_dtype) +
            (y_dtype == MOE_DT_F32 ? 3 : 1) * up256(static_cast<size_t>(B) * I * 2) +
-           std::max(part_bytes(B, H, I, 2, max_rank), part_bytes(B, I, H, 1, max_rank));
+           std::max(part_bytes(B, H, I, 2, max_rank, x_dtype), part_bytes(B, I, H, 1, max_rank, y_dtype));
 }
 
 hipError_t launch_lora_linear(ProjArgs a, void* ws, hipStream_t s) {
