@@ -238,12 +238,15 @@ __device__ __forceinline__ Picks route_exact(const GroupedArgs& a, const float (
 // largest possible score, a sum within half a unit of its size more.
 constexpr float kSigmoidErr = 0x1p-21f, kSoftmaxErr = 0x1p-19f;
 
-// One token: the wavefront's lanes hold its logits (masked ones -inf).
+// One token: the wavefront's lanes hold its logits (masked ones -inf) and
+// their experts' biases.  lds: kP * 64 doubles.
 template <int kP>
-__device__ __forceinline__ Picks route_token(const GroupedArgs& a, const float (&l)[kP], double* lds, int per,
-                                             int shift, uint32_t per_magic) {
+__device__ __forceinline__ Picks route_token(const GroupedArgs& a, const float (&l)[kP], const float (&bias)[kP],
+                                             double* lds, int per, int shift, uint32_t per_magic) {
     const int lane = threadIdx.x & (kWave - 1), e0 = kP * lane;
     const bool by_logit = a.bias == nullptr, sum2 = a.group_top2 && per > 1;
+    float* const val = reinterpret_cast<float*>(lds);       // group stage: the experts' values
+    float* const score = val + kP * kWave;                  // the experts' scores
     float s[kP];
     uint32_t key[kP];
     float err;   // of a score
@@ -256,7 +259,8 @@ __device__ __forceinline__ Picks route_token(const GroupedArgs& a, const float (
 #pragma unroll
         for (int j = 0; j < kP; ++j) {
             const float d = l[j] - m, b = d - l[j];   // l - m = d + (l - (d - b)) - (m + b), exactly
-            s[j] = l[j] > kNegInf ? exp_f32(d, (l[j] - (d - b)) - (m + b)) : 0.0f;
+            const float e = exp_f32(d, (l[j] - (d - b)) - (m + b));
+            s[j] = l[j] > kNegInf ? e : 0.0f;
             z += s[j];
         }
         const float inv = 1.0f / wave_sum(z);
@@ -265,20 +269,27 @@ __device__ __forceinline__ Picks route_token(const GroupedArgs& a, const float (
         err = kSoftmaxErr * inv;
     } else {
 #pragma unroll
-        for (int j = 0; j < kP; ++j) s[j] = l[j] > kNegInf ? __builtin_amdgcn_rcpf(1.0f + exp_f32(-l[j], 0.0f)) : 0.0f;
+        for (int j = 0; j < kP; ++j) {
+            const float v = __builtin_amdgcn_rcpf(1.0f + exp_f32(-l[j], 0.0f));
+            s[j] = l[j] > kNegInf ? v : 0.0f;
+        }
         err = kSigmoidErr;
     }
-    bool unsure = false;
-    float* val = reinterpret_cast<float*>(lds);
+    float c[kP];
 #pragma unroll
     for (int j = 0; j < kP; ++j) {
-        const int e = e0 + j;
-        float c = l[j];
-        if (!by_logit && c > kNegInf) c = s[j] + a.bias[e];
-        key[j] = key32(c);
-        if (a.n_group > 1 && e < a.N) val[e] = key[j] != 0u ? ((by_logit && sum2) ? s[j] : c) : kNegInf;
+        const float sum = s[j] + bias[j];
+        c[j] = (by_logit || !(l[j] > kNegInf)) ? l[j] : sum;
+        key[j] = key32(c[j]);
+        score[e0 + j] = s[j];
     }
+    bool unsure = false;
     if (a.n_group > 1) {
+#pragma unroll
+        for (int j = 0; j < kP; ++j) {
+            const float v = (by_logit && sum2) ? s[j] : c[j];
+            val[e0 + j] = key[j] != 0u ? v : kNegInf;
+        }
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         __builtin_amdgcn_wave_barrier();
         const float g = group_value(val, a, per, shift, sum2, lane);
@@ -292,17 +303,19 @@ __device__ __forceinline__ Picks route_token(const GroupedArgs& a, const float (
             }
             kept = __ballot(rank < a.topk_group);
         } else {
-            // groups surely and possibly above this one
+            // Groups surely and possibly above this one.  The margin is the same for all: a sum of two values and
+            // their difference's roundings, by the largest value in size (an infinity makes all unsure).
+            const bool live = g > kNegInf;
+            const float size = key_value(wave_max_u32(live ? key32(__builtin_fabsf(g)) : 0u));
+            const float margin = 4.0f * err + 0x1p-20f * size;
+            const float above = g + margin, below = g - margin;
             int sure = 0, maybe = 0;
-            const float slack = 4.0f * err + 0x1p-22f * __builtin_fabsf(g);
             for (int o = 0; o < a.n_group; ++o) {
                 const float v = lane_value(g, o << shift);
-                const float e = __builtin_fmaf(0x1p-22f, __builtin_fabsf(v), slack);
-                sure += v - g > e;
-                maybe += !(g - v > e) && o != mine;   // (also where an infinity leaves no difference)
+                sure += v > above;
+                maybe += !(v < below);
             }
-            const bool live = g > kNegInf;
-            const bool in = live && maybe < a.topk_group;
+            const bool in = live && maybe <= a.topk_group;   // (it counts itself)
             kept = __ballot(in);
             unsure = __any(mine < a.n_group && live && !in && sure < a.topk_group);
         }
@@ -314,45 +327,73 @@ __device__ __forceinline__ Picks route_token(const GroupedArgs& a, const float (
     }
     Picks out{-1, 0.0f, 0.0f};
     if (!unsure) {
-        float last = 0.0f, least = 1.0f;
-        for (int r = 0; r <= a.k; ++r) {   // the last round only compares
-            uint32_t best = key[0];
-            int bj = 0;
-            float bs = s[0];
+        // The lane's keys in descending order, equal ones as they were, with their experts in 16-bit fields of `order`: a
+        // lane's best is its first, and a pick moves its owner's list up.
+        uint32_t place[kP];
 #pragma unroll
-            for (int j = 1; j < kP; ++j) {
-                const bool up = key[j] > best;
-                best = up ? key[j] : best;
-                bj = up ? j : bj;
-                bs = up ? s[j] : bs;
+        for (int j = 0; j < kP; ++j) place[j] = j;
+#pragma unroll
+        for (int i = 0; i < kP - 1; ++i)
+#pragma unroll
+            for (int j = kP - 2; j >= i; --j) {
+                const bool up = key[j + 1] > key[j];
+                const uint32_t hi = max(key[j], key[j + 1]), lo = min(key[j], key[j + 1]);
+                const uint32_t p = up ? place[j + 1] : place[j], q = up ? place[j] : place[j + 1];
+                key[j] = hi;
+                key[j + 1] = lo;
+                place[j] = p;
+                place[j + 1] = q;
             }
-            const uint32_t top = wave_max_u32(best);
+        uint64_t order = 0ull;
+#pragma unroll
+        for (int j = 0; j < (kP < 4 ? kP : 4); ++j) order |= static_cast<uint64_t>(place[j] + e0) << (16 * j);
+        uint64_t order2 = 0ull;
+        if constexpr (kP > 4)
+#pragma unroll
+            for (int j = 4; j < kP; ++j) order2 |= static_cast<uint64_t>(place[j] + e0) << (16 * (j - 4));
+        float last = 0.0f;
+        int left = a.k;
+        for (int r = 0;; ++r, --left) {   // the last round only compares
+            const uint32_t top = wave_max_u32(key[0]);
             if (top == 0u) break;
             const float v = key_value(top);
-            if (!by_logit && r > 0 &&
-                !(last - v > 2.0f * err + 0x1p-22f * (__builtin_fabsf(last) + __builtin_fabsf(v)))) {
-                unsure = true;
-                break;
+            if (!by_logit) {
+                if (r > 0 && !(last - v > 2.0f * err + 0x1p-22f * (__builtin_fabsf(last) + __builtin_fabsf(v)))) {
+                    unsure = true;
+                    break;
+                }
+                last = v;
             }
-            last = v;
-            if (r == a.k) break;
-            const int owner = __ffsll(static_cast<unsigned long long>(__ballot(best == top))) - 1;
-            const int e = kP * owner + __builtin_amdgcn_readlane(bj, owner);
-            const float se = lane_value(bs, owner);
-            // two equal values: the lower index was taken; without a bias that is exact
+            if (left == 0) break;
+            const int owner = __ffsll(static_cast<unsigned long long>(__ballot(key[0] == top))) - 1;
+            const int e = __builtin_amdgcn_readlane(static_cast<int>(order), owner) & 0xffff;
+            out.e = lane == r ? e : out.e;
             const bool own = lane == owner;
 #pragma unroll
-            for (int j = 0; j < kP; ++j) key[j] = (own && j == bj) ? 0u : key[j];
-            out.e = lane == r ? e : out.e;
-            out.s = lane == r ? se : out.s;
-            out.sum += se;
-            least = fminf(least, se);
+            for (int j = 0; j + 1 < kP; ++j) key[j] = own ? key[j + 1] : key[j];
+            key[kP - 1] = own ? 0u : key[kP - 1];
+            if constexpr (kP > 1) {
+                uint64_t shifted = order >> 16;
+                if constexpr (kP > 4) {
+                    shifted |= order2 << 48;
+                    order2 = own ? order2 >> 16 : order2;
+                }
+                order = own ? shifted : order;
+            }
         }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        const bool filled = out.e >= 0;
+        out.s = score[filled ? out.e : 0];
         // scores near the end of fp32's range lose their ratio
-        unsure = unsure || least < 0x1p-100f;
+        unsure = unsure || __any(filled && out.s < 0x1p-100f);
+        out.s = filled ? out.s : 0.0f;
     }
     if (__builtin_amdgcn_readfirstlane(static_cast<int>(unsure))) return route_exact<kP>(a, l, lds, per, shift);
-    if (a.renorm) out.s = out.sum > 0.0f ? out.s / out.sum : 0.0f;
+    if (a.renorm) {
+        out.sum = wave_sum(out.s);
+        out.s = out.sum > 0.0f ? out.s / out.sum : 0.0f;
+    }
     return out;
 }
 
@@ -368,15 +409,18 @@ __global__ __launch_bounds__(W* kWave) void route_grouped_kernel(GroupedArgs a, 
     if (i < a.B) {   // whole wavefronts
         Picks p{-1, 0.0f, 0.0f};
         if (i < B_real) {
-            float l[kP];
+            float l[kP], bias[kP];
+#pragma unroll
+            for (int j = 0; j < kP; ++j) bias[j] = 0.0f;
+            if (a.bias != nullptr) load_logits<float, kP>(a.bias, a.N, kP * lane, (wide & 2) != 0, bias);
             load_logits<LT, kP>(static_cast<const LT*>(a.logits) + static_cast<size_t>(i) * a.N, a.N, kP * lane,
-                                wide != 0, l);
+                                (wide & 1) != 0, l);
 #pragma unroll
             for (int j = 0; j < kP; ++j) {   // NaN masks; +inf counts as the largest float
                 l[j] = l[j] > 3.402823466e38f ? 3.402823466e38f : l[j];
                 l[j] = l[j] > kNegInf ? l[j] : kNegInf;
             }
-            p = route_token<kP>(a, l, lds[wave], a.N / a.n_group, shift, per_magic);
+            p = route_token<kP>(a, l, bias, lds[wave], a.N / a.n_group, shift, per_magic);
         }
         if (lane < a.k) {
             a.idx[static_cast<size_t>(i) * a.k + lane] = p.e;
@@ -394,7 +438,10 @@ void launch(const GroupedArgs& a, hipStream_t s) {
     int shift = 6;   // lanes per group: 64 over n_group rounded up to a power of two
     while ((1 << (6 - shift)) < a.n_group) --shift;
     const uint32_t magic = ((1u << 20) + per - 1) / per;   // e / per = (e * magic) >> 20 for e < 512
-    const int wide = a.N % kP == 0 && reinterpret_cast<uintptr_t>(a.logits) % (sizeof(LT) * kP) == 0;
+    // rows of whole groups at aligned addresses: of the logits, of the bias
+    const int wide = a.N % kP != 0 ? 0
+                                   : (reinterpret_cast<uintptr_t>(a.logits) % (sizeof(LT) * kP) == 0 ? 1 : 0) +
+                                         (reinterpret_cast<uintptr_t>(a.bias) % (sizeof(float) * kP) == 0 ? 2 : 0);
     if (a.perm != nullptr) {
         if constexpr (kP <= 2)
             route_grouped_kernel<LT, kP, 16, true><<<(a.B + 15) / 16, 16 * kWave, 0, s>>>(a, shift, magic, wide);
