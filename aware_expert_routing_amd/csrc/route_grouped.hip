@@ -60,6 +60,21 @@ __device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) {
     v = max_dpp<0x143, 0xC>(v);
     return static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(v), kWave - 1));
 }
+// Maximum of floats none of which is NaN.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ float fmax_dpp(float v) {
+    return fmaxf(v, __int_as_float(__builtin_amdgcn_update_dpp(__float_as_int(v), __float_as_int(v), CTRL, ROWS, 0xF,
+                                                               false)));
+}
+__device__ __forceinline__ float wave_max(float v) {
+    v = fmax_dpp<0xB1, 0xF>(v);
+    v = fmax_dpp<0x4E, 0xF>(v);
+    v = fmax_dpp<0x141, 0xF>(v);
+    v = fmax_dpp<0x140, 0xF>(v);
+    v = fmax_dpp<0x142, 0xA>(v);
+    v = fmax_dpp<0x143, 0xC>(v);
+    return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), kWave - 1));
+}
 template <int CTRL>
 __device__ __forceinline__ float move_dpp(float v) {
     return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), CTRL, 0xF, 0xF, false));
@@ -148,6 +163,34 @@ __device__ __forceinline__ F group_value(const F* val, const GroupedArgs& a, int
         m2 = lo > hi2 ? lo : hi2;
     }
     return (sum2 && m2 > none) ? m1 + m2 : m1;
+}
+
+// The two largest of (m1 >= m2) and of a neighbour's pair, moved by a DPP control.
+template <int CTRL>
+__device__ __forceinline__ void merge_dpp(float& m1, float& m2) {
+    const float o1 = move_dpp<CTRL>(m1), o2 = move_dpp<CTRL>(m2);
+    m2 = fmaxf(fminf(m1, o1), fmaxf(m2, o2));
+    m1 = fmaxf(m1, o1);
+}
+// group_value where a group is 1 << shift whole lanes: no LDS.
+template <int kP>
+__device__ __forceinline__ float group_value_lanes(const float (&v)[kP], int shift, bool sum2) {
+    float m1 = v[0], m2 = kNegInf;
+#pragma unroll
+    for (int j = 1; j < kP; ++j) {
+        m2 = fmaxf(m2, fminf(m1, v[j]));
+        m1 = fmaxf(m1, v[j]);
+    }
+    if (shift > 0) merge_dpp<0xB1>(m1, m2);
+    if (shift > 1) merge_dpp<0x4E>(m1, m2);
+    if (shift > 2) merge_dpp<0x141>(m1, m2);
+    if (shift > 3) merge_dpp<0x140>(m1, m2);
+    for (int d = 16; d < (1 << shift); d <<= 1) {
+        const float o1 = __shfl_xor(m1, d, kWave), o2 = __shfl_xor(m2, d, kWave);
+        m2 = fmaxf(fminf(m1, o1), fmaxf(m2, o2));
+        m1 = fmaxf(m1, o1);
+    }
+    return (sum2 && m2 > kNegInf) ? m1 + m2 : m1;
 }
 
 // A token in 64 bits.
@@ -242,7 +285,7 @@ constexpr float kSigmoidErr = 0x1p-21f, kSoftmaxErr = 0x1p-19f;
 // their experts' biases.  lds: kP * 64 doubles.
 template <int kP>
 __device__ __forceinline__ Picks route_token(const GroupedArgs& a, const float (&l)[kP], const float (&bias)[kP],
-                                             double* lds, int per, int shift, uint32_t per_magic) {
+                                             double* lds, int per, int shift, int x_shift, uint32_t per_magic, bool g_lanes) {
     const int lane = threadIdx.x & (kWave - 1), e0 = kP * lane;
     const bool by_logit = a.bias == nullptr, sum2 = a.group_top2 && per > 1;
     float* const val = reinterpret_cast<float*>(lds);       // group stage: the experts' values
@@ -285,29 +328,34 @@ __device__ __forceinline__ Picks route_token(const GroupedArgs& a, const float (
     }
     bool unsure = false;
     if (a.n_group > 1) {
+        float gv[kP];
 #pragma unroll
-        for (int j = 0; j < kP; ++j) {
-            const float v = (by_logit && sum2) ? s[j] : c[j];
-            val[e0 + j] = key[j] != 0u ? v : kNegInf;
+        for (int j = 0; j < kP; ++j) gv[j] = key[j] != 0u ? ((by_logit && sum2) ? s[j] : c[j]) : kNegInf;
+        // a group as whole lanes (bands of 1 << shift of them from lane 0), or through LDS
+        float g;
+        if (g_lanes) {
+            g = group_value_lanes<kP>(gv, shift, sum2);
+        } else {
+#pragma unroll
+            for (int j = 0; j < kP; ++j) val[e0 + j] = gv[j];
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            __builtin_amdgcn_wave_barrier();
+            g = group_value(val, a, per, shift, sum2, lane);
         }
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        __builtin_amdgcn_wave_barrier();
-        const float g = group_value(val, a, per, shift, sum2, lane);
         const int mine = lane >> shift;
-        uint64_t kept;
+        bool in;
         if (by_logit && !sum2) {   // logits: exact
             int rank = 0;
             for (int o = 0; o < a.n_group; ++o) {
                 const float v = lane_value(g, o << shift);
                 rank += v > g || (v == g && o < mine);
             }
-            kept = __ballot(rank < a.topk_group);
+            in = rank < a.topk_group;
         } else {
             // Groups surely and possibly above this one.  The margin is the same for all: a sum of two values and
             // their difference's roundings, by the largest value in size (an infinity makes all unsure).
             const bool live = g > kNegInf;
-            const float size = key_value(wave_max_u32(live ? key32(__builtin_fabsf(g)) : 0u));
-            const float margin = 4.0f * err + 0x1p-20f * size;
+            const float margin = 4.0f * err + 0x1p-20f * wave_max(live ? __builtin_fabsf(g) : 0.0f);
             const float above = g + margin, below = g - margin;
             int sure = 0, maybe = 0;
             for (int o = 0; o < a.n_group; ++o) {
@@ -315,20 +363,25 @@ __device__ __forceinline__ Picks route_token(const GroupedArgs& a, const float (
                 sure += v > above;
                 maybe += !(v < below);
             }
-            const bool in = live && maybe <= a.topk_group;   // (it counts itself)
-            kept = __ballot(in);
+            in = live && maybe <= a.topk_group;   // (it counts itself)
             unsure = __any(mine < a.n_group && live && !in && sure < a.topk_group);
         }
+        if (g_lanes) {   // this lane's experts are in its band's group
 #pragma unroll
-        for (int j = 0; j < kP; ++j) {
-            const int group = static_cast<int>((static_cast<uint32_t>(e0 + j) * per_magic) >> 20);
-            if (e0 + j >= a.N || !((kept >> (group << shift)) & 1ull)) key[j] = 0u;
+            for (int j = 0; j < kP; ++j) key[j] = in && e0 + j < a.N ? key[j] : 0u;
+        } else {
+            const uint64_t kept = __ballot(in);
+#pragma unroll
+            for (int j = 0; j < kP; ++j) {
+                const int group = static_cast<int>((static_cast<uint32_t>(e0 + j) * per_magic) >> 20);
+                if (e0 + j >= a.N || !((kept >> (group << shift)) & 1ull)) key[j] = 0u;
+            }
         }
     }
     Picks out{-1, 0.0f, 0.0f};
     if (!unsure) {
-        // The lane's keys in descending order, equal ones as they were, with their experts in 16-bit fields of `order`: a
-        // lane's best is its first, and a pick moves its owner's list up.
+        // The lane's keys in descending order, equal ones as they were, each with its expert, in LDS: a lane's best
+        // is the one at its pointer, and a pick moves its owner's pointer on.
         uint32_t place[kP];
 #pragma unroll
         for (int j = 0; j < kP; ++j) place[j] = j;
@@ -344,52 +397,45 @@ __device__ __forceinline__ Picks route_token(const GroupedArgs& a, const float (
                 place[j] = p;
                 place[j + 1] = q;
             }
-        uint64_t order = 0ull;
+        uint32_t places = 0u;   // 4 bits each
 #pragma unroll
-        for (int j = 0; j < (kP < 4 ? kP : 4); ++j) order |= static_cast<uint64_t>(place[j] + e0) << (16 * j);
-        uint64_t order2 = 0ull;
-        if constexpr (kP > 4)
+        for (int j = 0; j < kP; ++j) places |= place[j] << (4 * j);
+        uint32_t* const sorted = reinterpret_cast<uint32_t*>(val);   // [kP][64]: the lane's j-th key
+        if constexpr (kP > 1) {
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            __builtin_amdgcn_wave_barrier();
 #pragma unroll
-            for (int j = 4; j < kP; ++j) order2 |= static_cast<uint64_t>(place[j] + e0) << (16 * (j - 4));
-        float last = 0.0f;
-        int left = a.k;
-        for (int r = 0;; ++r, --left) {   // the last round only compares
-            const uint32_t top = wave_max_u32(key[0]);
-            if (top == 0u) break;
-            const float v = key_value(top);
-            if (!by_logit) {
-                if (r > 0 && !(last - v > 2.0f * err + 0x1p-22f * (__builtin_fabsf(last) + __builtin_fabsf(v)))) {
-                    unsure = true;
-                    break;
-                }
-                last = v;
-            }
-            if (left == 0) break;
-            const int owner = __ffsll(static_cast<unsigned long long>(__ballot(key[0] == top))) - 1;
-            const int e = __builtin_amdgcn_readlane(static_cast<int>(order), owner) & 0xffff;
-            out.e = lane == r ? e : out.e;
-            const bool own = lane == owner;
-#pragma unroll
-            for (int j = 0; j + 1 < kP; ++j) key[j] = own ? key[j + 1] : key[j];
-            key[kP - 1] = own ? 0u : key[kP - 1];
-            if constexpr (kP > 1) {
-                uint64_t shifted = order >> 16;
-                if constexpr (kP > 4) {
-                    shifted |= order2 << 48;
-                    order2 = own ? order2 >> 16 : order2;
-                }
-                order = own ? shifted : order;
-            }
+            for (int j = 1; j < kP; ++j) sorted[j * kWave + lane] = key[j];
         }
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        __builtin_amdgcn_wave_barrier();
-        const bool filled = out.e >= 0;
+        uint32_t head = key[0], pick = 0u;   // pick: lane r's r-th key, and where it was
+        int from = 0, ptr = 0;
+        for (int r = 0; r <= a.k; ++r) {     // the last round is for the comparison behind the loop
+            const uint32_t top = wave_max_u32(head);
+            if (top == 0u) break;
+            const int owner = __ffsll(static_cast<unsigned long long>(__ballot(head == top))) - 1;
+            const bool own = lane == owner, here = lane == r;
+            const int at = __builtin_amdgcn_readlane(ptr, owner) * kWave + owner;
+            pick = here ? top : pick;
+            from = here ? at : from;
+            ptr += own ? 1 : 0;
+            const uint32_t next = ptr < kP ? sorted[min(ptr, kP - 1) * kWave + lane] : 0u;
+            head = own ? next : head;
+        }
+        // values of neighbouring picks have to differ by more than their errors (lane r + 1 holds the next one's)
+        const float v = key_value(pick), v1 = __shfl_down(v, 1, kWave);
+        const uint32_t pick1 = __shfl_down(pick, 1, kWave);
+        const bool close = !by_logit && lane < a.k && pick1 != 0u &&
+                           !(v - v1 > 2.0f * err + 0x1p-22f * (__builtin_fabsf(v) + __builtin_fabsf(v1)));
+        const bool filled = lane < a.k && pick != 0u;
+        const int owner = from & (kWave - 1);
+        const uint32_t p = __shfl(places, owner, kWave) >> (4 * (from >> 6));
+        out.e = filled ? kP * owner + static_cast<int>(p & 15u) : -1;
         out.s = score[filled ? out.e : 0];
         // scores near the end of fp32's range lose their ratio
-        unsure = unsure || __any(filled && out.s < 0x1p-100f);
+        unsure = __any(close || (filled && out.s < 0x1p-100f));
         out.s = filled ? out.s : 0.0f;
     }
-    if (__builtin_amdgcn_readfirstlane(static_cast<int>(unsure))) return route_exact<kP>(a, l, lds, per, shift);
+    if (__builtin_amdgcn_readfirstlane(static_cast<int>(unsure))) return route_exact<kP>(a, l, lds, per, x_shift);
     if (a.renorm) {
         out.sum = wave_sum(out.s);
         out.s = out.sum > 0.0f ? out.s / out.sum : 0.0f;
@@ -400,8 +446,8 @@ __device__ __forceinline__ Picks route_token(const GroupedArgs& a, const float (
 // W tokens per workgroup, one per wavefront.  kDispatch: the workgroup that
 // finishes last dispatches the batch (it counts in a.sync).
 template <typename LT, int kP, int W, bool kDispatch>
-__global__ __launch_bounds__(W* kWave) void route_grouped_kernel(GroupedArgs a, int shift, uint32_t per_magic,
-                                                                 int wide) {
+__global__ __launch_bounds__(W* kWave) void route_grouped_kernel(GroupedArgs a, int shift, int x_shift,
+                                                                 uint32_t per_magic, int flags) {
     __shared__ double lds[W][kP * kWave];
     const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
     const int i = blockIdx.x * W + wave;
@@ -412,15 +458,15 @@ __global__ __launch_bounds__(W* kWave) void route_grouped_kernel(GroupedArgs a, 
             float l[kP], bias[kP];
 #pragma unroll
             for (int j = 0; j < kP; ++j) bias[j] = 0.0f;
-            if (a.bias != nullptr) load_logits<float, kP>(a.bias, a.N, kP * lane, (wide & 2) != 0, bias);
+            if (a.bias != nullptr) load_logits<float, kP>(a.bias, a.N, kP * lane, (flags & 2) != 0, bias);
             load_logits<LT, kP>(static_cast<const LT*>(a.logits) + static_cast<size_t>(i) * a.N, a.N, kP * lane,
-                                (wide & 1) != 0, l);
+                                (flags & 1) != 0, l);
 #pragma unroll
             for (int j = 0; j < kP; ++j) {   // NaN masks; +inf counts as the largest float
                 l[j] = l[j] > 3.402823466e38f ? 3.402823466e38f : l[j];
                 l[j] = l[j] > kNegInf ? l[j] : kNegInf;
             }
-            p = route_token<kP>(a, l, bias, lds[wave], a.N / a.n_group, shift, per_magic);
+            p = route_token<kP>(a, l, bias, lds[wave], a.N / a.n_group, shift, x_shift, per_magic, (flags & 4) != 0);
         }
         if (lane < a.k) {
             a.idx[static_cast<size_t>(i) * a.k + lane] = p.e;
@@ -435,18 +481,24 @@ __global__ __launch_bounds__(W* kWave) void route_grouped_kernel(GroupedArgs a, 
 template <typename LT, int kP>
 void launch(const GroupedArgs& a, hipStream_t s) {
     const int per = a.N / a.n_group;
-    int shift = 6;   // lanes per group: 64 over n_group rounded up to a power of two
-    while ((1 << (6 - shift)) < a.n_group) --shift;
+    int x_shift = 6;   // lanes per group: 64 over n_group rounded up to a power of two
+    while ((1 << (6 - x_shift)) < a.n_group) --x_shift;
+    int shift = x_shift, g_lanes = 0;   // or a group's own lanes, where it is a power of two of whole ones
+    if (per % kP == 0 && ((per / kP) & (per / kP - 1)) == 0) {
+        g_lanes = 4;
+        shift = __builtin_ctz(per / kP);
+    }
     const uint32_t magic = ((1u << 20) + per - 1) / per;   // e / per = (e * magic) >> 20 for e < 512
     // rows of whole groups at aligned addresses: of the logits, of the bias
     const int wide = a.N % kP != 0 ? 0
                                    : (reinterpret_cast<uintptr_t>(a.logits) % (sizeof(LT) * kP) == 0 ? 1 : 0) +
                                          (reinterpret_cast<uintptr_t>(a.bias) % (sizeof(float) * kP) == 0 ? 2 : 0);
+    const int flags = wide + g_lanes;
     if (a.perm != nullptr) {
         if constexpr (kP <= 2)
-            route_grouped_kernel<LT, kP, 16, true><<<(a.B + 15) / 16, 16 * kWave, 0, s>>>(a, shift, magic, wide);
+            route_grouped_kernel<LT, kP, 16, true><<<(a.B + 15) / 16, 16 * kWave, 0, s>>>(a, shift, x_shift, magic, flags);
     } else {
-        route_grouped_kernel<LT, kP, 4, false><<<(a.B + 3) / 4, 4 * kWave, 0, s>>>(a, shift, magic, wide);
+        route_grouped_kernel<LT, kP, 4, false><<<(a.B + 3) / 4, 4 * kWave, 0, s>>>(a, shift, x_shift, magic, flags);
     }
 }
 
