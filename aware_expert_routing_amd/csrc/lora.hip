@@ -855,26 +855,33 @@ __global__ __launch_bounds__(kFinishWaves* kWave) void proj_finish_kernel(ProjAr
     const int B_real = real_tokens(a);
     if (16 * tt >= B_real) return;
     const int i = 16 * tt + n;
-    f32x4 acc[T];   // block m RBF + j
+    // The list, then the wave's first part: both on their way while the adapters' operands are fetched.
+    u32x4 items[NM];   // lane l holds the wave's item l: one load for the whole list
+    int count[NM], most = 0;
 #pragma unroll
-    for (int p = 0; p < T; ++p) acc[p] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    for (int sp = wave; sp < g.parts; sp += W)
-#pragma unroll
-        for (int p = 0; p < T; ++p)
-            acc[p] += g.part[(((static_cast<size_t>(sp) * NM + p / RBF) * tt_all + tt) * blocks +
-                              min(ob0 + p % RBF, blocks - 1)) * kWave + lane];
+    for (int m = 0; m < NM; ++m) count[m] = 0;
     if (g.list_wgs > 0) {
-        const size_t row = static_cast<size_t>(min(i, B_real - 1)) * a.max_rank;
-        // lane l holds the wave's item l: one load for the whole list
-        u32x4 items[NM];
-        int count[NM], most = 0;
 #pragma unroll
         for (int m = 0; m < NM; ++m) {
             const size_t at = (static_cast<size_t>(m) * tt_all + tt) * W + __builtin_amdgcn_readfirstlane(wave);
             items[m] = *reinterpret_cast<const u32x4*>(g.items + at * kMaxItems + min(lane, kMaxItems - 1));
             count[m] = g.n_items[at];
-            most = max(most, count[m]);
         }
+    }
+    auto part_at = [&](int sp, int p) {
+        return g.part[(((static_cast<size_t>(sp) * NM + p / RBF) * tt_all + tt) * blocks +
+                       min(ob0 + p % RBF, blocks - 1)) * kWave + lane];
+    };
+    f32x4 acc[T], first[T];   // block m RBF + j
+#pragma unroll
+    for (int p = 0; p < T; ++p) {
+        acc[p] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        first[p] = wave < g.parts ? part_at(wave, p) : acc[p];
+    }
+    if (g.list_wgs > 0) {
+        const size_t row = static_cast<size_t>(min(i, B_real - 1)) * a.max_rank;
+#pragma unroll
+        for (int m = 0; m < NM; ++m) most = max(most, count[m]);
         for (int d0 = 0; d0 < most; d0 += D) {   // D items of each matrix, whose loads are in flight together
             u32x2 b[NM][D][RBF];
             f32x4 v[NM][D];
@@ -919,6 +926,11 @@ __global__ __launch_bounds__(kFinishWaves* kWave) void proj_finish_kernel(ProjAr
                 }
         }
     }
+#pragma unroll
+    for (int p = 0; p < T; ++p) acc[p] += first[p];
+    for (int sp = wave + W; sp < g.parts; sp += W)
+#pragma unroll
+        for (int p = 0; p < T; ++p) acc[p] += part_at(sp, p);
     fold_waves<W>(part, acc, wave, lane);
     const int ob = ob0 + wave;
     if (wave >= RBF || ob >= blocks || i >= B_real) return;
