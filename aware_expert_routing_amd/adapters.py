@@ -12,7 +12,9 @@ from . import _lib as L
 
 
 class LoraTable:
-    """n adapters of a projection [O, H], each of rank at most max_rank."""
+    """n adapters of a projection [O, H], each of rank at most max_rank, none
+    published yet (the table is cleared on the current stream; another stream
+    that publishes into it or reads it has to come after that)."""
 
     def __init__(self, n: int, H: int, O: int, max_rank: int, device="cuda"):
         if n < 1:

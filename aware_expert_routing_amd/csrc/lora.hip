@@ -10,8 +10,24 @@
 // product's C layout (lane = 16 q + n holds ranks 4 q .. 4 q + 3 of token n)
 // is the second's B operand layout.
 //
-// Two launches: `shrink` forms v_i = s_a A_a x_i in fp32, and the projection
-// adds B_a v_i to its accumulators before it stores.
+// v_i = s_a A_a x_i is formed in fp32 first, and B_a v_i is added before the
+// outputs are stored.  By sizes (plan_proj):
+//   few tokens with few rank blocks   one launch (proj_fused_kernel)
+//   a decode batch                    the product split over its columns, beside
+//                                     it v and the lists of adapters, in one
+//                                     launch (proj_split_kernel); the sums, B v
+//                                     and the epilogue in a second one
+//                                     (proj_finish_kernel)
+//   many tokens                       v (shrink_kernel), then a tiled product
+//                                     that adds B v behind its columns
+//                                     (proj_tile_kernel)
+// Few tokens are bound by latency and by what one compute unit can have in
+// flight, a decode batch by the weights' way from memory and the two launches,
+// many tokens by the matrix units.  Measured on an MI355X, kernel time, with
+// adapters: 1 token of 2048 x 2048 5.7 us (weights alone at the copy rate of
+// 4.8 TB/s: 1.8); 64 tokens of 4096 x 4096 with 24 adapters 21 us (9.7); 4096
+// tokens of 4096 x 4096 with 8 adapters 143 us, without 117, where the matrix
+// units' rate in a large library product (1.40 PFLOP/s) gives 98.
 //
 // Precision: products are bf16 x bf16 with fp32 sums.  An fp32 value enters as
 // three bf16 terms cut from its 24 significant bits (exact); v enters an fp32
@@ -42,12 +58,13 @@ __device__ __forceinline__ f32x4 mma16(u32x2 a, u32x2 b, f32x4 c) {
 }
 
 // The leading 8 significant bits of f as a float, and what is left (0 for an
-// infinity, whose difference to itself is NaN).
+// infinity, whose difference to itself is NaN; a NaN stays one, also where its
+// set bits all lie in the lower half).
 __device__ __forceinline__ float cut8(float f, float& rest) {
     const float t = __uint_as_float(__float_as_uint(f) & 0xffff0000u);
     const float r = f - t;
     rest = r == r ? r : 0.0f;
-    return t;
+    return f == f ? t : __uint_as_float(0x7fc00000u);
 }
 __device__ __forceinline__ uint32_t pair_hi(float a, float b) {   // bf16 bits of a (low half) and b
     return __builtin_amdgcn_perm(__float_as_uint(b), __float_as_uint(a), 0x07060302u);
@@ -1153,9 +1170,10 @@ __global__ __launch_bounds__(WR* WC* kWave, 2) void proj_tile_kernel(ProjArgs a,
     }
 }
 
-// fp32 rows cut into their three bf16 terms, as planes.
-__global__ __launch_bounds__(256) void planes_kernel(const f32x4* __restrict__ x, long chunks, u32x2* __restrict__ out,
-                                                     size_t plane) {
+// fp32 rows (the real tokens') cut into their three bf16 terms, as planes.
+__global__ __launch_bounds__(256) void planes_kernel(ProjArgs a, u32x2* __restrict__ out, size_t plane) {
+    const f32x4* x = static_cast<const f32x4*>(a.x);
+    const long chunks = static_cast<long>(real_tokens(a)) * a.H / 4;
     for (long c = static_cast<long>(blockIdx.x) * blockDim.x + threadIdx.x; c < chunks;
          c += static_cast<long>(gridDim.x) * blockDim.x) {
         const f32x4 v = x[c];
@@ -1382,7 +1400,7 @@ hipError_t cut_x(ProjArgs& a, void* ws, hipStream_t s) {
     const size_t plane = up256(static_cast<size_t>(a.B) * a.H * 2);
     const long chunks = static_cast<long>(a.B) * a.H / 4;
     planes_kernel<<<static_cast<unsigned>(std::min<long>((chunks + 255) / 256, 4096)), 256, 0, s>>>(
-        static_cast<const f32x4*>(a.x), chunks, static_cast<u32x2*>(ws), plane);
+        a, static_cast<u32x2*>(ws), plane);
     a.x = ws;
     a.x_kind = kActPlanes;
     a.x_plane = plane;

@@ -322,3 +322,55 @@ def test_packed_adapters_round_trip():
                 b[l % 16::16, 4 * (l // 16) + j::16] = pb[:, :, l, j]
         assert np.array_equal(a[:rank], A.view(torch.int16).numpy()) and not a[rank:].any()
         assert np.array_equal(b[:, :rank], B.view(torch.int16).numpy()) and not b[:, rank:].any()
+
+
+@pytest.mark.parametrize("B", [7, 40, 200, 700])
+def test_nan_patterns_of_fp32_rows(B):
+    # a NaN whose set mantissa bits all lie below the bf16 half is still a NaN, in its row alone
+    H, O = 256, 96
+    W, x = _weights(95, O, H), _acts(96, B, H, "f32")
+    x.view(torch.int32)[3, 17] = 0x7F800001
+    y = moe.lora_linear(x.to(DEV), _pack(W))
+    rows = [i for i in range(B) if i != 3]
+    assert torch.isnan(y[3]).all()
+    _check_linear(y[rows], x[rows], W, None, None, "f32")
+
+
+@pytest.mark.parametrize("B", [1, 24, 300])
+def test_graph_replays_follow_table_ids_and_rows(B):
+    H, O, n = 512, 272, 5
+    entries = lora_ref.make_table(100, n, H, O, (16, 24))
+    W = _weights(101, O, H)
+    t, w = _table(entries, H, O, 32), _pack(W)
+    x = torch.zeros(B, H, device=DEV)
+    ids = torch.full((B,), -1, device=DEV, dtype=torch.int32)
+    y = torch.zeros(B, O, device=DEV)
+    n_valid = torch.tensor([B], device=DEV, dtype=torch.int32)
+    ws = torch.empty(moe.lora_workspace_bytes(B, H, O, 32, torch.float32, torch.float32), device=DEV, dtype=torch.uint8)
+
+    def call():
+        moe.lora_linear(x, w, t, ids, y=y, ws=ws, n_valid=n_valid)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        call()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    for step, nv in enumerate((B, max(1, B // 2), 0, B)):
+        xs, idx = _acts(110 + step, B, H, "f32"), _ids(120 + step, B, n)
+        x.copy_(xs)
+        ids.copy_(idx)
+        n_valid.fill_(nv)
+        y.fill_(3.0)
+        if step == 3:   # another adapter under the same handle
+            entries[2] = lora_ref.make_table(130, 1, H, O, (32,))[0]
+            t.publish(2, entries[2][0].to(DEV), entries[2][1].to(DEV), entries[2][2])
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.all(y[nv:] == 3.0)
+        if nv:
+            _check_linear(y[:nv], xs[:nv], W, entries, idx[:nv], "f32")
