@@ -1387,6 +1387,12 @@ size_t v_bytes(int B, int max_rank) { return up256(static_cast<size_t>(B) * max_
 size_t x_planes_bytes(int B, int H, int x_dtype) {   // fp32 x of more than kRowTokens tokens
     return x_dtype == MOE_DT_F32 && B > kRowTokens ? 3 * up256(static_cast<size_t>(B) * H * 2) : 0;
 }
+// How the shared expert's h is kept: as the three terms of its fp32 value for
+// an fp32 y, and for a bf16 y of up to 32 tokens, which are bound by latency;
+// beyond, rounded to bf16 once, as y is (101 tokens of H = 1344, I = 1280: 25 us
+// against 32 with three terms).
+bool h_is_cut(int B, bool y_f32) { return y_f32 || B <= 32; }
+
 // Partial blocks and item lists of a projection: the most any number of
 // adapters asks for.
 size_t part_bytes(int B, int H, int O, int mats, int max_rank, int x_dtype) {
@@ -1414,12 +1420,14 @@ size_t lora_workspace_bytes(int B, int H, int O, int max_rank, int x_dtype) {
     return v_bytes(B, max_rank) + x_planes_bytes(B, H, x_dtype) + part_bytes(B, H, O, 1, max_rank, x_dtype);
 }
 
-// v of gate, up and down, the planes of x, h (bf16, or three planes for an
-// fp32 y), partial blocks of the larger projection.
+// v of gate, up and down, the planes of x, h (bf16 or three planes), partial
+// blocks of the larger projection.
 size_t shared_ffn_workspace_bytes(int B, int H, int I, int max_rank, int x_dtype, int y_dtype) {
+    const bool cut = h_is_cut(B, y_dtype == MOE_DT_F32);
     return 3 * v_bytes(B, max_rank) + x_planes_bytes(B, H, x_dtype) +
-           (y_dtype == MOE_DT_F32 ? 3 : 1) * up256(static_cast<size_t>(B) * I * 2) +
-           std::max(part_bytes(B, H, I, 2, max_rank, x_dtype), part_bytes(B, I, H, 1, max_rank, y_dtype));
+           (cut ? 3 : 1) * up256(static_cast<size_t>(B) * I * 2) +
+           std::max(part_bytes(B, H, I, 2, max_rank, x_dtype),
+                    part_bytes(B, I, H, 1, max_rank, cut ? MOE_DT_F32 : MOE_DT_BF16));
 }
 
 hipError_t launch_lora_linear(ProjArgs a, void* ws, hipStream_t s) {
@@ -1442,7 +1450,7 @@ hipError_t launch_shared_ffn(ProjArgs a, const void* w_down, const moe_lora_hand
     char* x_planes = p + 3 * vb;
     char* h = x_planes + x_planes_bytes(a.B, a.H, a.x_kind == kActF32 ? MOE_DT_F32 : MOE_DT_BF16);
     a.y = h;
-    a.y_kind = a.y_kind == kActF32 ? kActPlanes : kActBf16;
+    a.y_kind = h_is_cut(a.B, a.y_kind == kActF32) ? kActPlanes : kActBf16;
     a.y_plane = h_plane;
     a.accumulate = 0;
     d.w[0] = w_down;

@@ -390,9 +390,10 @@ int moe_lora_linear(const void *w, const moe_lora_handle *table, int n_adapters,
  *            moe_expert_ffn (gate, up [I, H], down [H, I])
  *   t_gate, t_up, t_down : adapter tables of the three projections, any of
  *            them NULL; one adapter id per token serves all three
- * The remaining arguments and rules are those of moe_lora_linear.  h is kept
- * in y's type: fp32 (three terms in the down projection), or rounded to bf16
- * where y is bf16.  H and I multiples of 32, at most 16384.
+ * The remaining arguments and rules are those of moe_lora_linear.  h enters
+ * the down projection with all 24 bits (three terms) where y is fp32 or
+ * B <= 32; for a bf16 y of more tokens it is rounded to bf16 once, as y is.
+ * H and I multiples of 32, at most 16384.
  */
 size_t moe_shared_ffn_workspace_bytes(int B, int H, int I, int max_rank, int x_dtype, int y_dtype);
 int moe_shared_ffn(const moe_expert_handle *shared, const moe_lora_handle *t_gate, const moe_lora_handle *t_up,
