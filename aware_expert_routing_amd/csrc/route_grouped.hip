@@ -103,8 +103,10 @@ __device__ __forceinline__ uint64_t wave_max_u64(uint64_t v) {
 
 // exp(x + lo) within 2 units of fp32: x log2(e) in two pieces, the second
 // applied to the result's first order.  x is held to [-100, 88], where every
-// step is finite (a score that this touches is below 2^-100).
+// step is finite (a score that this touches is below 2^-100); there lo does not
+// count (the difference of two logits that ends at -inf has none).
 __device__ __forceinline__ float exp_f32(float x, float lo) {
+    lo = x > -100.0f ? lo : 0.0f;
     x = fminf(fmaxf(x, -100.0f), 88.0f);
     const float y = x * 1.44269502f;                       // log2(e), fp32
     const float r = __builtin_fmaf(x, 1.44269502f, -y) + __builtin_fmaf(x, 1.92596300e-8f, lo * 1.44269502f);
@@ -195,7 +197,8 @@ __device__ __forceinline__ float group_value_lanes(const float (&v)[kP], int shi
 
 // A token in 64 bits.
 template <int kP>
-__device__ __forceinline__ Picks route_exact(const GroupedArgs& a, const float (&l_in)[kP], double* val, int per, int shift) {
+__device__ __forceinline__ Picks route_exact(const GroupedArgs& a, const float (&l_in)[kP], double* val, int per,
+                                             int shift) {
     const int lane = threadIdx.x & (kWave - 1), e0 = kP * lane;
     const bool by_logit = a.bias == nullptr, sum2 = a.group_top2 && per > 1;
     double s[kP], c[kP];
@@ -285,7 +288,8 @@ constexpr float kSigmoidErr = 0x1p-21f, kSoftmaxErr = 0x1p-19f;
 // their experts' biases.  lds: kP * 64 doubles.
 template <int kP>
 __device__ __forceinline__ Picks route_token(const GroupedArgs& a, const float (&l)[kP], const float (&bias)[kP],
-                                             double* lds, int per, int shift, int x_shift, uint32_t per_magic, bool g_lanes) {
+                                             double* lds, int per, int shift, int x_shift, uint32_t per_magic,
+                                             bool g_lanes) {
     const int lane = threadIdx.x & (kWave - 1), e0 = kP * lane;
     const bool by_logit = a.bias == nullptr, sum2 = a.group_top2 && per > 1;
     float* const val = reinterpret_cast<float*>(lds);       // group stage: the experts' values
@@ -496,7 +500,8 @@ void launch(const GroupedArgs& a, hipStream_t s) {
     const int flags = wide + g_lanes;
     if (a.perm != nullptr) {
         if constexpr (kP <= 2)
-            route_grouped_kernel<LT, kP, 16, true><<<(a.B + 15) / 16, 16 * kWave, 0, s>>>(a, shift, x_shift, magic, flags);
+            route_grouped_kernel<LT, kP, 16, true>
+                <<<(a.B + 15) / 16, 16 * kWave, 0, s>>>(a, shift, x_shift, magic, flags);
     } else {
         route_grouped_kernel<LT, kP, 4, false><<<(a.B + 3) / 4, 4 * kWave, 0, s>>>(a, shift, x_shift, magic, flags);
     }

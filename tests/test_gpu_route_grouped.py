@@ -111,6 +111,21 @@ def test_masked_experts_and_empty_rows(score, bias):
             _check(idx, w, *grouped_ref.route_grouped(logits, k, score, b, G, tg, gs, renorm, 2.0))
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_differences_of_logits_past_the_largest_float(score):
+    # l - max overflows to -inf: such an expert scores 0 and stays selectable
+    low = np.finfo(np.float32).min
+    logits, _ = _inputs(79, 4, 32, False)
+    logits[0, 7], logits[0, 9:25] = np.inf, low
+    logits[1, ::2], logits[1, 1] = low, np.float32(2e38)
+    logits[2], logits[2, 3] = low, np.inf
+    logits[3, :8] = np.linspace(-3e38, 3e38, 8).astype(np.float32)
+    for renorm in (True, False):
+        idx, w = moe.route_grouped(_dev(logits), 6, score=score, n_group=4, topk_group=3, group_score="max",
+                                   renorm=renorm)
+        _check(idx, w, *grouped_ref.route_grouped(logits, 6, score, None, 4, 3, "max", renorm, 1.0))
+
+
 def test_large_logits_keep_their_order():
     # sigmoid scores that are all 0 or 1 to fp32: without a bias the logits rank the experts
     logits = (synth.normal(3, (6, 40), 1.0) * np.float32(60)).astype(np.float32)
