@@ -17,7 +17,8 @@ OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmoe.so")
 ARCH = "gfx950"
 
-SOURCES = ["abi.cpp", "residency.cpp", "route.hip", "route_grouped.hip", "ffn.hip", "lora.hip", "quant.hip", "pack.hip", "probe.hip"]
+SOURCES = ["abi.cpp", "residency.cpp", "route.hip", "route_grouped.hip", "ffn.hip", "lora.hip",
+           "quant.hip", "pack.hip", "probe.hip"]
 NO_CONTRACT = {"route.hip", "route_grouped.hip", "quant.hip"}
 
 COMMON = ["-O3", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-Wall", "-Wno-unused-function",

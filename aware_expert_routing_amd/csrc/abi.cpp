@@ -343,7 +343,8 @@ MOE_API int moe_lora_publish(moe_lora_handle* table, int i, const moe_lora_handl
     if (h->rank > moe::kMaxLoraRank) return fail(MOE_EUNSUPPORTED, "rank above 256 is not supported");
     if (h->rank > 0) {
         if (!h->a || !h->b) return fail(MOE_EINVAL, "null adapter pointer");
-        if (misaligned(h->a, 16) || misaligned(h->b, 16)) return fail(MOE_EINVAL, "packed adapters must be 16-byte aligned");
+        if (misaligned(h->a, 16) || misaligned(h->b, 16))
+            return fail(MOE_EINVAL, "packed adapters must be 16-byte aligned");
         if (!(h->scale - h->scale == 0.0f)) return fail(MOE_EINVAL, "scale must be finite");
     }
     return hip_status(moe::launch_lora_publish(table, i, *h, as_stream(stream)), "moe_lora_publish");
@@ -363,13 +364,15 @@ MOE_API int moe_lora_linear(const void* w, const moe_lora_handle* table, int n_a
     a.w[0] = w; a.table[0] = table; a.adapter = table ? adapter : nullptr;
     a.n_adapters = n_adapters; a.max_rank = table ? max_rank : 0;
     a.x = x; a.x_kind = x_dtype == MOE_DT_F32 ? moe::kActF32 : moe::kActBf16; a.B = B; a.H = H; a.O = O;
-    a.n_valid = n_valid; a.y = y; a.y_kind = y_dtype == MOE_DT_F32 ? moe::kActF32 : moe::kActBf16; a.accumulate = accumulate != 0;
+    a.n_valid = n_valid; a.y = y; a.y_kind = y_dtype == MOE_DT_F32 ? moe::kActF32 : moe::kActBf16;
+    a.accumulate = accumulate != 0;
     int st = check_proj(a, x_dtype, y_dtype, table != nullptr);
     if (st) return st;
     if (H < 32 || H % 32) return fail(MOE_EINVAL, "H must be a positive multiple of 32");
     if (O < 16 || O % 16) return fail(MOE_EINVAL, "O must be a positive multiple of 16");
     if (H > 16384 || O > 16384) return fail(MOE_EUNSUPPORTED, "H and O above 16384 are not supported");
-    if (misaligned(w, 16) || misaligned(table, 16)) return fail(MOE_EINVAL, "w and the handle table must be 16-byte aligned");
+    if (misaligned(w, 16) || misaligned(table, 16))
+        return fail(MOE_EINVAL, "w and the handle table must be 16-byte aligned");
     st = check_workspace(ws, ws_bytes, moe_lora_workspace_bytes(B, H, O, a.max_rank, x_dtype, y_dtype));
     if (st) return st;
     return hip_status(moe::launch_lora_linear(a, ws, as_stream(stream)), "moe_lora_linear");
@@ -398,7 +401,8 @@ MOE_API int moe_shared_ffn(const moe_expert_handle* shared, const moe_lora_handl
     a.adapter = any ? adapter : nullptr;
     a.n_adapters = n_adapters; a.max_rank = any ? max_rank : 0;
     a.x = x; a.x_kind = x_dtype == MOE_DT_F32 ? moe::kActF32 : moe::kActBf16; a.B = B; a.H = H; a.O = I;
-    a.n_valid = n_valid; a.y = y; a.y_kind = y_dtype == MOE_DT_F32 ? moe::kActF32 : moe::kActBf16; a.accumulate = accumulate != 0;
+    a.n_valid = n_valid; a.y = y; a.y_kind = y_dtype == MOE_DT_F32 ? moe::kActF32 : moe::kActBf16;
+    a.accumulate = accumulate != 0;
     int st = check_proj(a, x_dtype, y_dtype, any);
     if (st) return st;
     if (H < 32 || H % 32 || I < 32 || I % 32) return fail(MOE_EINVAL, "H and I must be positive multiples of 32");

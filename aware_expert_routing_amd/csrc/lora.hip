@@ -1145,7 +1145,9 @@ __global__ __launch_bounds__(WR* WC* kWave, 2) void proj_tile_kernel(ProjArgs a,
             for (int j = 0; j < MB; ++j)
 #pragma unroll
                 for (int t = 0; t < NB; ++t) acc[t / 4][j][t % 4] = mma32(w[j], x0[t], acc[t / 4][j][t % 4]);
-        wait_and_barrier<0>();   // no copy may land in the next plane's ring, or after the workgroup's end
+        // No copy may land in the next plane's ring, or after the workgroup's end, and none of the next plane's
+        // before a wave has its last operands.
+        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
     }
 #pragma unroll
     for (int h = 0; h < Q; ++h) {
@@ -1278,7 +1280,8 @@ hipError_t launch_proj(const ProjArgs& a, void* part, hipStream_t s) {
     Plan p = plan_proj(a.B, a.H, a.O, NM, a.adapter != nullptr ? rank_blocks_bound(a.B, a.n_adapters, a.max_rank) : 0,
                        XK == kActBf16 ? 1 : 3);
     if (p.path == kFused) {
-        // 16 waves where each has four steps and more (H = 2048, one token: 5.7 against 6.3 us; H = 768: 4.7 against 4.1)
+        // 16 waves where each has four steps and more (H = 2048, one token: 5.7 against 6.3 us; H = 768: 4.7 against
+        // 4.1)
         if (a.H >= 2048) proj_fused_kernel<XK, YK, NM, 16, 4><<<a.O / 16, 16 * kWave, 0, s>>>(a);
         else proj_fused_kernel<XK, YK, NM, 8, 4><<<a.O / 16, 8 * kWave, 0, s>>>(a);
         return hipGetLastError();

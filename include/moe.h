@@ -14,8 +14,9 @@
  *   - The caller owns every buffer.  Buffers must not overlap unless stated.
  *   - Limits: 1 <= N <= 128 experts, 1 <= k <= min(N, 16), 1 <= B <= 128;
  *     grouped routing, the projections and the shared expert state their own.
- *   - Non-finite logits (except in grouped routing), and idx entries outside [-1, N) or repeated within a
- *     token's row, are undefined behaviour (not checked on the device).
+ *   - Non-finite logits (except in grouped routing), and idx entries outside
+ *     [-1, N) or repeated within a token's row, are undefined behaviour (not
+ *     checked on the device).
  *
  * Page citations
  *   [OEA]  "Opportunistic Expert Activation (OEA) - L2" (zhaifeiyue.github.io)
@@ -227,8 +228,10 @@ int moe_router_route_dispatch(const void *x, int x_dtype, const float *w_r, int 
  *   one).  The topk_group best groups stay, the k best experts in them are
  *   taken; w = s_e (without the bias), divided by the sum over the kept
  *   experts when renorm != 0 (all 0 if that sum is 0), times scale.  Ties go
- *   to the lower index.  Scores, selection values and sums are formed in 64
- *   bits and w is rounded once.
+ *   to the lower index.  idx is what 64-bit scores, selection values and sums
+ *   give; w lies within 2^-18 of its 64-bit value, relative to it (fp32 sums
+ *   and exponentials with bounded errors; tokens whose choice those cannot
+ *   decide are formed in 64 bits).
  *   Masked experts: a NaN or -inf logit, or a NaN or -inf bias, keeps an
  *   expert from being picked (a masked logit adds nothing to the softmax);
  *   +inf counts as the largest float.  A token with fewer than k selectable
