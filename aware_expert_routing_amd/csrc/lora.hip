@@ -26,8 +26,11 @@
 // many tokens by the matrix units.  Measured on an MI355X, kernel time, with
 // adapters: 1 token of 2048 x 2048 5.7 us (weights alone at the copy rate of
 // 4.8 TB/s: 1.8); 64 tokens of 4096 x 4096 with 24 adapters 21 us (9.7); 4096
-// tokens of 4096 x 4096 with 8 adapters 143 us, without 117, where the matrix
-// units' rate in a large library product (1.40 PFLOP/s) gives 98.
+// tokens of 4096 x 4096 with 8 adapters 134 us, without 117, where the matrix
+// units' rate in a large library product (1.40 PFLOP/s) gives 98.  The shared
+// expert: 1 token of H = 2048, I = 768 with an adapter 13 us (2.0), 128 of 4096,
+// 1536 with 24 adapters 60 (15), 2999 of the same with 6 adapters 175 alone and
+// 152 where calls follow each other (82).
 //
 // Precision: products are bf16 x bf16 with fp32 sums.  An fp32 value enters as
 // three bf16 terms cut from its 24 significant bits (exact); v enters an fp32

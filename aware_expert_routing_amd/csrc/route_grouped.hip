@@ -13,13 +13,23 @@
 // closer than an fp32 rounding at the border of a choice, and such a pair
 // would be picked by the rounding of the exponential.  They are taken in fp32
 // where that is certain: every value carries a bound on its error, and a token
-// with a comparison inside the bounds (about one in a hundred) is routed again
-// in 64 bits by its wavefront.
+// with a comparison inside the bounds (one or two in a thousand: 256 experts,
+// k = 8) is routed again in 64 bits by its wavefront.  All in 64 bits, 16384
+// such tokens took 71 us; this way 24.
 //
 // One wavefront per token; lane l owns the kP consecutive experts from kP l,
 // so that of equal values the lowest lane, and in it the first, is the lower
 // index.  A selection is a lane-local maximum over order keys and a 6-step DPP
-// maximum.  Group values go through LDS once (group sizes are the caller's).
+// maximum.  A lane sorts its keys first, so that a pick moves one pointer in
+// place of kP comparisons.  Group values stay in registers where a group is a
+// power of two of whole lanes, and go through LDS otherwise.
+//
+// Bounds: a few tokens by the chain of selections (k = 8: 4.3 us for one
+// token's kernel, 5.8 for 77 of 160 experts), many by the vector units: 16384
+// tokens of 256 fp32 logits, 18 MB, in 24 us, 0.75 TB/s, where a copy of as
+// much takes 3.7.  The dispatching form (128 tokens of 128 experts, 8.6 us) runs
+// 16 tokens in a workgroup, so that few have to finish before the last one
+// dispatches.
 #include "dispatch.h"
 #include "internal.h"
 
