@@ -374,3 +374,34 @@ def test_graph_replays_follow_table_ids_and_rows(B):
         assert torch.all(y[nv:] == 3.0)
         if nv:
             _check_linear(y[:nv], xs[:nv], W, entries, idx[:nv], "f32")
+
+
+def _far_rows(B):   # the first rows, those round 2^32 bytes of 16 KB rows, and the last
+    return torch.cat([torch.arange(20), torch.arange(2 ** 18 - 20, 2 ** 18 + 20), torch.arange(B - 20, B)])
+
+
+@pytest.mark.parametrize("xdt,ydt", [("bf16", "bf16"), ("f32", "f32")])
+@pytest.mark.parametrize("H,O", [(32, 8192), (8192, 32)])
+def test_offsets_past_32_bits(H, O, xdt, ydt):
+    B = 2 ** 18 + 1001   # rows of 16 KB (bf16): x, its planes or y pass 4 GiB
+    g = torch.Generator(device=DEV).manual_seed(B + H)
+    x = torch.randn(B, H, generator=g, device=DEV, dtype=DT[xdt])
+    entries = lora_ref.make_table(5, 3, H, O, (8, 20))
+    W, ids = _weights(H, O, H), _ids(6, B, 3)
+    y = moe.lora_linear(x, _pack(W), _table(entries, H, O), ids.to(DEV), y_dtype=DT[ydt])
+    at = _far_rows(B)
+    _check_linear(y[at.to(DEV)], x[at.to(DEV)].cpu(), W, entries, ids[at], ydt)
+
+
+@pytest.mark.parametrize("ydt", ["bf16", "f32"])
+def test_shared_expert_whose_h_passes_32_bits(ydt):
+    B, H, I = 2 ** 18 + 1001, 32, 8192
+    ws, tabs, _, _ = _shared(31, 1, H, I, 2, (8,), "bf16")
+    g = torch.Generator(device=DEV).manual_seed(32)
+    x = torch.randn(B, H, generator=g, device=DEV, dtype=torch.bfloat16)
+    ids = _ids(33, B, 2)
+    sh = moe.ExpertTensors.pack(moe.MOE_W_BF16, *[w.to(DEV) for w in ws])
+    loras = [_table(t, *hw) for t, hw in zip(tabs, [(H, I), (H, I), (I, H)])]
+    y = moe.shared_ffn(x, sh, loras, ids.to(DEV), y_dtype=DT[ydt])
+    at = _far_rows(B)
+    _check_shared(y[at.to(DEV)], x[at.to(DEV)].cpu(), ws, tabs, ids[at], ydt)

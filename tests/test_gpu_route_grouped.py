@@ -244,3 +244,14 @@ def test_tensors_are_checked():
         moe.route_grouped(x, 65)
     with pytest.raises(moe.MoeError):
         moe.route_grouped(x, 4, n_group=5)
+
+
+def test_offsets_past_32_bits():
+    B, N = 2 ** 20, 512   # the largest call: 2 GiB of fp32 logits
+    gen = torch.Generator(device=DEV).manual_seed(7)
+    logits = torch.randn(B, N, generator=gen, device=DEV) * 1.5
+    _, bias = _inputs(81, 1, N, True)
+    idx, w = moe.route_grouped(logits, 32, bias=_dev(bias), n_group=8, topk_group=4, scale=2.5)
+    at = torch.cat([torch.arange(20), torch.arange(B // 2 - 20, B // 2 + 20), torch.arange(B - 20, B)]).to(DEV)
+    ref = grouped_ref.route_grouped(logits[at].cpu().numpy(), 32, "sigmoid", bias, 8, 4, "top2", True, 2.5)
+    _check(idx[at], w[at], *ref)
